@@ -33,6 +33,8 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_BIAS_LOGIT = 0
 MOE_BIAS_SELECT = 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
+MOE_GATE_LINEAR, MOE_GATE_SIGMOID = 0, 1
 
 DECODE_MAX_TOKENS = 8
 
@@ -57,11 +59,69 @@ class moe_route_out(C.Structure):
     _fields_ = [("topk_idx", C.c_void_p), ("topk_w", C.c_void_p), ("expert_counts", C.c_void_p)]
 
 
+def _struct(name, *groups):
+    """A ctypes structure whose first field, struct_size, fills itself."""
+    fields = [("struct_size", C.c_uint32)] + [(f, t) for t, names in groups for f in names.split()]
+
+    def init(self, *a, **k):
+        C.Structure.__init__(self, C.sizeof(type(self)), *a, **k)
+
+    return type(name, (C.Structure,), {"_fields_": fields, "__init__": init})
+
+
+moe_norm_out_args = _struct(
+    "moe_norm_out_args",
+    (C.c_int32, "n_tokens d_model o_dtype res_dtype res_out_dtype w_dtype gate_dtype h_dtype gate_kind gate_act unit_offset"),
+    (C.c_float, "eps next_eps scale"),
+    (C.c_void_p, "o residual weight gate res_out next_weight h"),
+    (C.c_int64, "o_stride res_stride gate_stride res_out_stride h_stride"))
+moe_norm_in_bwd_args = _struct(
+    "moe_norm_in_bwd_args",
+    (C.c_int32, "n_tokens d_model x_dtype w_dtype dh_dtype dres_dtype dx_dtype unit_offset"),
+    (C.c_float, "eps"),
+    (C.c_void_p, "x weight dh dres dx dweight workspace"),
+    (C.c_uint64, "workspace_bytes"),
+    (C.c_int64, "x_stride dh_stride dres_stride dx_stride"))
+moe_norm_out_bwd_args = _struct(
+    "moe_norm_out_bwd_args",
+    (C.c_int32, "n_tokens d_model o_dtype w_dtype gate_dtype dres_dtype gate_kind gate_act unit_offset"),
+    (C.c_float, "eps scale"),
+    (C.c_void_p, "o weight gate dres d_o dweight dgate workspace"),
+    (C.c_uint64, "workspace_bytes"),
+    (C.c_int64, "o_stride gate_stride dres_stride do_stride dgate_stride"))
+moe_adapters_config = _struct(
+    "moe_adapters_config", (C.c_int32, "d_in d_out max_adapters max_rank max_tokens device"))
+moe_ffn_args = _struct(
+    "moe_ffn_args",
+    (C.c_int32, "n_tokens d_model d_ff add_dtype y_dtype"),
+    (C.c_void_p, "x w_gate w_up w_down add y save_gate save_up workspace"),
+    (C.c_uint64, "workspace_bytes"),
+    (C.c_int64, "x_stride add_stride y_stride"))
+moe_ffn_bwd_args = _struct(
+    "moe_ffn_bwd_args",
+    (C.c_int32, "n_tokens d_model d_ff"),
+    (C.c_void_p, "dy x w_gate w_up w_down save_gate save_up dx dw_gate dw_up dw_down workspace"),
+    (C.c_uint64, "workspace_bytes"),
+    (C.c_int64, "dy_stride x_stride dx_stride"))
+moe_block = _struct(
+    "moe_block",
+    (C.c_int32, "norm_dtype"),
+    (C.c_void_p, "norm_in_w norm_out_w gate"),
+    (C.c_float, "norm_in_eps norm_out_eps scale"),
+    (C.c_int32, "gate_act unit_offset ffn_d_ff"),
+    (C.c_void_p, "ffn_gate ffn_up ffn_down adapters"))
+
+
 EXPORTED = [
     "moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack", "moe_check", "moe_destroy",
     "moe_status_string", "moe_last_error", "moe_device_bytes", "moe_debug_set_spin_limit",
     "moe_debug_set_alloc_cap", "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read",
     "moe_route_noalloc",
+    "moe_norm_in", "moe_norm_out", "moe_norm_workspace", "moe_norm_in_backward", "moe_norm_out_backward",
+    "moe_adapters_create", "moe_adapters_load", "moe_adapters_apply", "moe_adapters_check", "moe_adapters_destroy",
+    "moe_adapters_last_error", "moe_adapters_device_bytes",
+    "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_check",
+    "moe_blocks_workspace", "moe_forward_blocks",
 ]
 
 _lib = None
@@ -97,6 +157,33 @@ def lib() -> C.CDLL:
         L.moe_profile_enable.argtypes = [P, I]
         L.moe_profile_read.argtypes = [P, I, C.POINTER(C.c_float), C.POINTER(I)]
         L.moe_route_noalloc.argtypes = [P, I, P, I, I, I, P, I, I, P, P, P]
+        I64, F = C.c_int64, C.c_float
+        L.moe_norm_in.argtypes = [P, I, I64, P, I, F, I, P, I, I64, I, I, P]
+        for name in ("moe_norm_out", "moe_norm_in_backward", "moe_norm_out_backward", "moe_ffn_forward",
+                     "moe_ffn_backward"):
+            getattr(L, name).argtypes = [P, P]
+        L.moe_norm_workspace.argtypes = [I, I]
+        L.moe_norm_workspace.restype = U64
+        L.moe_adapters_create.argtypes = [P, C.POINTER(P)]
+        L.moe_adapters_load.argtypes = [P, I, P, P, I, F, P]
+        L.moe_adapters_apply.argtypes = [P, P, I, I64, P, I64, P, I64, I, P, I, P]
+        L.moe_adapters_check.argtypes = [P]
+        L.moe_adapters_destroy.argtypes = [P]
+        L.moe_adapters_last_error.argtypes = [P]
+        L.moe_adapters_last_error.restype = C.c_char_p
+        L.moe_adapters_device_bytes.argtypes = [P]
+        L.moe_adapters_device_bytes.restype = U64
+        L.moe_ffn_workspace.argtypes = [I, I, I, I]
+        L.moe_ffn_workspace.restype = U64
+        L.moe_ffn_check.argtypes = []
+        L.moe_blocks_workspace.argtypes = [P, P, I, I]
+        L.moe_blocks_workspace.restype = U64
+        L.moe_forward_blocks.argtypes = [P, I, I, P, P, P, I, P, P, U64, P, C.POINTER(moe_route_out)]
+        for name in ("moe_norm_in", "moe_norm_out", "moe_norm_in_backward", "moe_norm_out_backward",
+                     "moe_adapters_create", "moe_adapters_load", "moe_adapters_apply", "moe_adapters_check",
+                     "moe_adapters_destroy", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_check",
+                     "moe_forward_blocks"):
+            getattr(L, name).restype = I
         for name in ("moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack", "moe_check",
                      "moe_destroy", "moe_debug_set_spin_limit", "moe_debug_set_alloc_cap",
                      "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read", "moe_route_noalloc"):
@@ -247,6 +334,32 @@ class MoE:
         self._check(moe_forward_stack(self.h, first_layer, n_layers, _ptr(x_in), _ptr(x_out), n, _stream(), arr,
                                       _ptr(x_trace)), "moe_forward_stack")
 
+    def forward_blocks(self, first_layer, blocks, x_in, x_out, adapter_ids=None, routes=None):
+        """Layers first_layer .. with their norms, gates, dense blocks and adapters: one ``Block`` per layer
+        (``moe_forward_blocks`` in include/moe.h).  The workspace of the dense blocks comes from PyTorch."""
+        import torch
+
+        from . import block as B
+
+        dev = torch.device("cuda", self.cfg.device)
+        n, nl, d = x_in.shape[0], len(blocks), self.cfg.d_model
+        B.matrix(x_in, "x_in", dev, (None, d), dtype=B.TYPES[self.cfg.act_dtype], dense=True)
+        B.matrix(x_out, "x_out", dev, (n, d), dtype=B.TYPES[self.cfg.out_dtype], dense=True)
+        if adapter_ids is not None:
+            B.vector(adapter_ids, "adapter_ids", dev, n, torch.int32)
+        arr = (moe_block * nl)(*[b.args(d, dev) for b in blocks])
+        nbytes = lib().moe_blocks_workspace(self.h, arr, nl, n)
+        r = None
+        if routes is not None:
+            if len(routes) != nl:
+                raise ValueError("routes: one entry per layer")
+            r = (moe_route_out * nl)(*[moe_route_out(*[_ptr(q.get(k)) for k in ("idx", "w", "counts")]) for q in routes])
+        with torch.cuda.device(dev):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+            self._check(lib().moe_forward_blocks(self.h, first_layer, nl, arr, x_in.data_ptr(), x_out.data_ptr(), n,
+                                                 _ptr(adapter_ids), _ptr(ws), nbytes, _stream(), r),
+                        "moe_forward_blocks")
+
     def check(self) -> int:
         return moe_check(self.h)
 
@@ -263,3 +376,17 @@ class MoE:
             self.close()
         except Exception:
             pass
+
+
+# The block operators' wrappers (block.py) need torch, which this module only imports when it is used.
+_BLOCK = ("norm_in", "norm_out", "norm_in_backward", "norm_out_backward", "Adapters", "ffn_forward", "ffn_backward",
+          "ffn_check", "Block")
+
+
+def __getattr__(name):
+    if name not in _BLOCK:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import block
+
+    globals().update({k: getattr(block, k) for k in _BLOCK})
+    return globals()[name]

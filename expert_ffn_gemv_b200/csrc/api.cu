@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <vector>
 
+#include "block.cuh"
 #include "moe_internal.cuh"
 #include "prefill.cuh"
 
@@ -678,6 +679,98 @@ moe_status moe_forward_stack(moe_handle *h, int32_t first_layer, int32_t n_layer
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(h, e, "stream synchronize");
     return check_device_error(h, st);
+  }
+  return MOE_OK;
+}
+
+uint64_t moe_blocks_workspace(const moe_handle *h, const moe_block *blocks, int32_t n_layers, int32_t n_tokens) {
+  if (!h || !blocks) return 0;
+  uint64_t most = 0;
+  for (int i = 0; i < n_layers; ++i)
+    if (blocks[i].ffn_d_ff > 0)
+      most = std::max<uint64_t>(most, moe_ffn_workspace(n_tokens, h->cfg.d_model, blocks[i].ffn_d_ff, 0));
+  return most;
+}
+
+moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_layers, const moe_block *blocks,
+                              const void *x_in, void *x_out, int32_t n_tokens, const int32_t *adapter_ids,
+                              void *workspace, uint64_t workspace_bytes, void *stream, moe_route_out *per_layer_route) {
+  if (!h) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config &g = h->cfg;
+  if (!blocks || !x_in || !x_out || x_in == x_out || n_tokens < 1 || n_tokens > g.max_tokens || n_layers < 1 ||
+      first_layer < 0 || first_layer > g.n_layers - n_layers)
+    return fail(h, MOE_ERR_INVALID_ARGUMENT, "bad block arguments");
+  DeviceGuard guard(g.device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!is_device_ptr(x_in) || !is_device_ptr(x_out))
+    return fail(h, MOE_ERR_INVALID_ARGUMENT, "x_in and x_out must be device memory");
+  const int D = g.d_model;
+  for (int i = 0; i < n_layers; ++i) {
+    const moe_block &b = blocks[i];
+    if (b.struct_size != sizeof(moe_block) || !b.norm_in_w || b.ffn_d_ff < 0 ||
+        (b.norm_dtype != MOE_F32 && b.norm_dtype != MOE_BF16))
+      return fail(h, MOE_ERR_INVALID_ARGUMENT, "bad block description");
+    if (b.ffn_d_ff && (g.act_dtype != MOE_BF16 || !b.ffn_gate || !b.ffn_up || !b.ffn_down))
+      return fail(h, MOE_ERR_INVALID_ARGUMENT, "a dense block needs bf16 activations and its three matrices");
+    if (b.adapters && !adapter_ids) return fail(h, MOE_ERR_INVALID_ARGUMENT, "adapter_ids is missing");
+    if (b.adapters && !adapters_match(b.adapters, D, g.device, n_tokens))
+      return fail(h, MOE_ERR_INVALID_ARGUMENT, "the adapters' sizes, device or max_tokens do not fit");
+  }
+  if (workspace_bytes < moe_blocks_workspace(h, blocks, n_layers, n_tokens))
+    return fail(h, MOE_ERR_INVALID_ARGUMENT, "workspace too small");
+  moe_status s = check_device_error(h, st);
+  if (s != MOE_OK) return s;
+  for (int l = first_layer; l < first_layer + n_layers; ++l)
+    if (!h->layers[l].loaded) return fail(h, MOE_ERR_NOT_LOADED, "layer not loaded");
+  // the block input a and the block output o (fp32) take the staging buffers, x the residual buffer
+  void *a = h->x_stage;
+  float *o = static_cast<float *>(h->y_stage), *res = h->res[0];
+  s = moe_norm_in(x_in, g.act_dtype, D, blocks[0].norm_in_w, blocks[0].norm_dtype, blocks[0].norm_in_eps,
+                  blocks[0].unit_offset, a, g.act_dtype, D, n_tokens, D, stream);
+  if (s != MOE_OK) return fail(h, s, "input norm");
+  for (int i = 0; i < n_layers; ++i) {
+    const moe_block &b = blocks[i];
+    const bool last = i == n_layers - 1;
+    s = run_layer(h, first_layer + i, a, g.act_dtype == MOE_BF16, o, 0, n_tokens, 0, nullptr,
+                  per_layer_route ? per_layer_route + i : nullptr, st, first_layer + i);
+    if (s != MOE_OK) return s;
+    if (b.ffn_d_ff) {
+      moe_ffn_args f{};
+      f.struct_size = sizeof f;
+      f.n_tokens = n_tokens, f.d_model = D, f.d_ff = b.ffn_d_ff;
+      f.x = a, f.x_stride = D;
+      f.w_gate = b.ffn_gate, f.w_up = b.ffn_up, f.w_down = b.ffn_down;
+      f.add = o, f.add_dtype = MOE_F32, f.add_stride = D;
+      f.y = o, f.y_dtype = MOE_F32, f.y_stride = D;
+      f.workspace = workspace, f.workspace_bytes = workspace_bytes;
+      if ((s = moe_ffn_forward(&f, stream)) != MOE_OK) return fail(h, s, "dense block");
+    }
+    if (b.adapters) {
+      s = moe_adapters_apply(b.adapters, a, g.act_dtype, D, o, D, o, D, MOE_F32, adapter_ids, n_tokens, stream);
+      if (s != MOE_OK) return fail(h, s, std::string("adapters: ") + moe_adapters_last_error(b.adapters));
+    }
+    moe_norm_out_args q{};
+    q.struct_size = sizeof q;
+    q.n_tokens = n_tokens, q.d_model = D;
+    q.o = o, q.o_dtype = MOE_F32, q.o_stride = D;
+    q.residual = i ? res : x_in, q.res_dtype = i ? MOE_F32 : g.act_dtype, q.res_stride = D;
+    q.weight = b.norm_out_w, q.w_dtype = b.norm_dtype, q.eps = b.norm_out_eps, q.unit_offset = b.unit_offset;
+    q.gate = b.gate, q.gate_kind = b.gate ? MOE_GATE_CHANNEL : MOE_GATE_NONE, q.gate_act = b.gate_act;
+    q.gate_dtype = b.norm_dtype, q.scale = b.scale;
+    q.res_out = last ? x_out : res, q.res_out_dtype = last ? g.out_dtype : MOE_F32, q.res_out_stride = D;
+    // the next block's input norm in the same pass where its weights have this block's type and offset
+    const bool fuse = !last && blocks[i + 1].norm_dtype == b.norm_dtype && blocks[i + 1].unit_offset == b.unit_offset;
+    if (fuse) {
+      q.next_weight = blocks[i + 1].norm_in_w, q.next_eps = blocks[i + 1].norm_in_eps;
+      q.h = a, q.h_dtype = g.act_dtype, q.h_stride = D;
+    }
+    if ((s = moe_norm_out(&q, stream)) != MOE_OK) return fail(h, s, "output norm");
+    if (!last && !fuse) {
+      const moe_block &nb = blocks[i + 1];
+      s = moe_norm_in(res, MOE_F32, D, nb.norm_in_w, nb.norm_dtype, nb.norm_in_eps, nb.unit_offset, a, g.act_dtype, D,
+                      n_tokens, D, stream);
+      if (s != MOE_OK) return fail(h, s, "input norm");
+    }
   }
   return MOE_OK;
 }

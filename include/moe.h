@@ -188,6 +188,188 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
                              int32_t x_dtype, int32_t n_tokens, int32_t *topk_idx, float *topk_w,
                              void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Block operators: what stands around and beside the routed experts in a transformer layer.  Norms
+ * before and after a block with gate and residual scale, low-rank adapters of many requests, and a
+ * dense gated feed-forward block from bf16 weights (a layer, or a shared block, that is not kept
+ * in low-bit blocks), with the gradients of the norms and of the dense block (they are local to a
+ * layer, so a quantised layer can be tuned against its original with the routed experts frozen).
+ * All of them take device pointers, run on the current device (adapters: on their handle's),
+ * enqueue on `stream`, never synchronise the host and allocate nothing, so they can be captured
+ * into a CUDA graph.  Strides count values between the starts of consecutive rows.  Each result is
+ * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
+ * Outputs may not overlap inputs unless said so.
+ * ------------------------------------------------------------------------------------------- */
+/* What a gate is broadcast over: one value per column, per token, or of its own for every value. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
+/* a(g) = g, or sigmoid(g) */
+typedef enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 } moe_gate_act;
+
+/* Norm before a block: h_t = x_t / sqrt(mean(x_t^2) + eps) * (weight + unit_offset).
+ * x, h: n_tokens x d_model (x_dtype, h_dtype); h may be x when types and strides agree.
+ * d_model 1..8192 (larger: UNSUPPORTED), n_tokens >= 1, eps >= 0, unit_offset 0 or 1. */
+moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype, float eps,
+                       int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride, int32_t n_tokens,
+                       int32_t d_model, void *stream);
+
+/* Norm after a block, its gate, the residual scale and add, and (h != NULL) the next block's input
+ * norm in the same pass:
+ *   u = o / sqrt(mean(o^2) + eps) * (weight + unit_offset)      (weight NULL: u = o)
+ *   res_out = residual + scale * a(gate) * u                    (no gate: a = 1)
+ *   h = res_out / sqrt(mean(res_out^2) + next_eps) * (next_weight + unit_offset)
+ * h is computed from res_out as it is stored, so it equals moe_norm_in of res_out.  res_out may be
+ * residual or o, and h may be o, when types and strides agree. */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(moe_norm_out_args) */
+  int32_t n_tokens, d_model;
+  int32_t o_dtype, res_dtype, res_out_dtype, w_dtype, gate_dtype, h_dtype; /* moe_dtype */
+  int32_t gate_kind, gate_act, unit_offset;
+  float eps, next_eps, scale;
+  const void *o;             /* n_tokens x d_model: the block's output */
+  const void *residual;      /* n_tokens x d_model */
+  const void *weight;        /* d_model, w_dtype, or NULL */
+  const void *gate;          /* by gate_kind: d_model; n_tokens; n_tokens x d_model; NULL */
+  void *res_out;             /* n_tokens x d_model */
+  const void *next_weight;   /* d_model, w_dtype; NULL iff h is NULL */
+  void *h;                   /* n_tokens x d_model, or NULL */
+  int64_t o_stride, res_stride, gate_stride, res_out_stride, h_stride; /* gate: token and full */
+} moe_norm_out_args;
+moe_status moe_norm_out(const moe_norm_out_args *args, void *stream);
+
+/* Bytes of workspace that either backward call needs (0: sizes out of range). */
+uint64_t moe_norm_workspace(int32_t n_tokens, int32_t d_model);
+
+/* Gradients of moe_norm_in: dx = dres + (dh's gradient through the norm), dweight = sum over tokens.
+ * dres (or NULL): a gradient that reaches x another way, e.g. over the residual; dx may be dres. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_tokens, d_model;
+  int32_t x_dtype, w_dtype, dh_dtype, dres_dtype, dx_dtype, unit_offset;
+  float eps;
+  const void *x, *weight, *dh, *dres;
+  void *dx;
+  void *dweight;             /* d_model, w_dtype, or NULL */
+  void *workspace;           /* 16-byte aligned; not needed when dweight is NULL */
+  uint64_t workspace_bytes;
+  int64_t x_stride, dh_stride, dres_stride, dx_stride;
+} moe_norm_in_bwd_args;
+moe_status moe_norm_in_backward(const moe_norm_in_bwd_args *args, void *stream);
+
+/* Gradients of moe_norm_out (without h) from dres = the gradient of res_out, which is the gradient
+ * of residual as it stands: d_o (o_dtype), dweight and dgate (the gate's shape and type; dgate_stride
+ * for token and full). */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_tokens, d_model;
+  int32_t o_dtype, w_dtype, gate_dtype, dres_dtype;
+  int32_t gate_kind, gate_act, unit_offset;
+  float eps, scale;
+  const void *o, *weight, *gate, *dres;
+  void *d_o;
+  void *dweight;             /* or NULL */
+  void *dgate;               /* or NULL */
+  void *workspace;           /* 16-byte aligned; for dweight and a channel gate's dgate */
+  uint64_t workspace_bytes;
+  int64_t o_stride, gate_stride, dres_stride, do_stride, dgate_stride;
+} moe_norm_out_bwd_args;
+moe_status moe_norm_out_backward(const moe_norm_out_bwd_args *args, void *stream);
+
+/* Low-rank adapters of many requests:  out_t = base_t + scale_i B_i (A_i x_t) with i = ids[t], and
+ * out_t = base_t where ids[t] = -1.  The handle owns the adapters (repacked) and a workspace; like
+ * a moe_handle it serves one stream at a time, captured graphs included. */
+typedef struct moe_adapters moe_adapters; /* opaque */
+typedef struct {
+  uint32_t struct_size;   /* sizeof(moe_adapters_config) */
+  int32_t d_in, d_out;    /* multiples of 8, 8..65536 */
+  int32_t max_adapters;   /* slots, 1..4096 */
+  int32_t max_rank;       /* 1..128 */
+  int32_t max_tokens;     /* per call, 1..8192 */
+  int32_t device;
+} moe_adapters_config;
+moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **out);
+/* Put an adapter into a slot (replacing what is there, in stream order): a rank x d_in and b
+ * d_out x rank, bf16, row-major, host or device (host sources: the call waits for the copy).
+ * rank 0 (a, b NULL) empties the slot. */
+moe_status moe_adapters_load(moe_adapters *h, int32_t slot, const void *a, const void *b, int32_t rank, float scale,
+                             void *stream);
+/* x: n_tokens x d_in (x_dtype); base, out: n_tokens x d_out (out_dtype); out may be base (same
+ * stride), then rows without an adapter are not touched.  ids: n_tokens slots on the device.
+ * Pointers and row strides must be multiples of 16 bytes.  An id that is out of range or names an
+ * empty slot counts as -1 and makes the next call (or moe_adapters_check) return
+ * MOE_ERR_DEVICE_FAULT. */
+moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, int64_t x_stride, const void *base,
+                              int64_t base_stride, void *out, int64_t out_stride, int32_t out_dtype, const int32_t *ids,
+                              int32_t n_tokens, void *stream);
+moe_status moe_adapters_check(moe_adapters *h);
+moe_status moe_adapters_destroy(moe_adapters *h);
+const char *moe_adapters_last_error(const moe_adapters *h);
+uint64_t moe_adapters_device_bytes(const moe_adapters *h);
+
+/* Dense gated feed-forward block, bf16 weights: y = w_down (silu(w_gate x) * (w_up x)) (+ add).
+ * d_model and d_ff: multiples of 8, 8..65536; every pointer 16-byte aligned, every row stride a
+ * multiple of 16 bytes.  The hidden values are kept in bf16 between the products. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_tokens, d_model, d_ff;
+  int32_t add_dtype, y_dtype;
+  const void *x;                       /* n_tokens x d_model, bf16 */
+  const void *w_gate, *w_up, *w_down;  /* d_ff x d_model, d_ff x d_model, d_model x d_ff, bf16 */
+  const void *add;                     /* n_tokens x d_model added to the result, or NULL; may be y */
+  void *y;                             /* n_tokens x d_model */
+  void *save_gate, *save_up;           /* for the backward: w_gate x and w_up x, n_tokens x d_ff
+                                          fp32, or both NULL */
+  void *workspace;                     /* moe_ffn_workspace(.., 0) bytes, used by one call at a time */
+  uint64_t workspace_bytes;
+  int64_t x_stride, add_stride, y_stride;
+} moe_ffn_args;
+uint64_t moe_ffn_workspace(int32_t n_tokens, int32_t d_model, int32_t d_ff, int32_t backward);
+moe_status moe_ffn_forward(const moe_ffn_args *args, void *stream);
+
+/* Its gradients from dy (of the block alone: the gradient of add is dy itself).  All outputs bf16;
+ * dx, the pair dw_gate / dw_up and dw_down may each be NULL, not all of them. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_tokens, d_model, d_ff;
+  const void *dy, *x;                  /* n_tokens x d_model, bf16 */
+  const void *w_gate, *w_up, *w_down;
+  const void *save_gate, *save_up;     /* of the forward call */
+  void *dx;                            /* n_tokens x d_model */
+  void *dw_gate, *dw_up, *dw_down;     /* the weights' shapes */
+  void *workspace;                     /* moe_ffn_workspace(.., 1) bytes */
+  uint64_t workspace_bytes;
+  int64_t dy_stride, x_stride, dx_stride;
+} moe_ffn_bwd_args;
+moe_status moe_ffn_backward(const moe_ffn_bwd_args *args, void *stream);
+/* Synchronises the current device and returns (and clears) a pending MOE_ERR_TIMEOUT of the dense
+ * block's kernels there: a bounded wait ran out and the call's results are not valid. */
+moe_status moe_ffn_check(void);
+
+/* A run of layers first_layer .. first_layer + n_layers - 1 with everything that stands around and
+ * beside their routed experts, x kept in fp32 between the layers:
+ *   a = norm_in(x)            o = MoE_l(a) (+ dense block(a)) (+ adapters(a))
+ *   x = x + scale * act(gate) * norm_out(o)
+ * One moe_block per layer; the caller keeps what it points to (device memory) alive. */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(moe_block) */
+  int32_t norm_dtype;        /* of the norm weights and the gate */
+  const void *norm_in_w;     /* d_model, required */
+  const void *norm_out_w;    /* d_model, or NULL: no norm after the block */
+  const void *gate;          /* d_model values (one per column), or NULL */
+  float norm_in_eps, norm_out_eps, scale;
+  int32_t gate_act, unit_offset;
+  int32_t ffn_d_ff;          /* dense block beside the experts: its d_ff, 0: none */
+  const void *ffn_gate, *ffn_up, *ffn_down;
+  moe_adapters *adapters;    /* d_in = d_out = d_model, or NULL */
+} moe_block;
+/* Bytes of workspace for these blocks (0 when no layer has a dense block). */
+uint64_t moe_blocks_workspace(const moe_handle *h, const moe_block *blocks, int32_t n_layers, int32_t n_tokens);
+/* x_in: act_dtype, x_out: out_dtype, device memory, not aliased.  adapter_ids: n_tokens slots, or NULL
+ * when no layer has adapters.  A dense block needs act_dtype = MOE_BF16.  Errors as
+ * moe_forward_stack, and those of the operators. */
+moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_layers, const moe_block *blocks,
+                              const void *x_in, void *x_out, int32_t n_tokens, const int32_t *adapter_ids,
+                              void *workspace, uint64_t workspace_bytes, void *stream, moe_route_out *per_layer_route);
+
 /* Test hooks.  moe_debug_set_spin_limit: clock cycles a device-side bounded wait may spin
  * before it gives up (0 restores the default of about one second).  moe_debug_set_alloc_cap:
  * fail allocations that would take the handle above `bytes` (0 = no cap). */
