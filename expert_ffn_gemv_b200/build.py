@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library libmoe_b200.so in-tree (nvcc, no JIT cache).
+"""Build the sm_100a shared library libmoe_b200.so in-tree (nvcc, no JIT cache), and the host-side
+binding of its block operators for torch tensors, _block_ext.so (g++).
 
     python -m expert_ffn_gemv_b200.build        # or: import expert_ffn_gemv_b200.build as b; b.build()
 """
@@ -22,6 +23,36 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxe
          "-I", str(ROOT / "include"), "-I", str(CSRC)]
 
 
+# CPython binding of the block operators for torch tensors (host code, built against the installed torch)
+EXT = OUT_DIR / "_block_ext.so"
+EXT_SOURCES = [CSRC / "bind.cpp", ROOT / "include" / "moe.h"]
+
+
+def build_ext(force: bool = False) -> Path:
+    if not force and EXT.exists() and all(p.stat().st_mtime <= EXT.stat().st_mtime for p in EXT_SOURCES):
+        return EXT
+    import sysconfig
+
+    from torch.utils import cpp_extension as ce
+
+    OUT_DIR.mkdir(exist_ok=True)
+    cuda = str(Path(nvcc()).resolve().parent.parent / "include")
+    inc = [*ce.include_paths(), cuda, sysconfig.get_paths()["include"], str(ROOT / "include")]
+    import torch
+
+    libs = Path(torch.__file__).parent / "lib"
+    tmp = EXT.with_suffix(f".{os.getpid()}.tmp")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{i}" for i in inc], str(CSRC / "bind.cpp"), "-o", str(tmp),
+           f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def nvcc() -> str:
     cand = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     return cand
@@ -31,7 +62,7 @@ def _stale() -> bool:
     if not LIB.exists():
         return True
     t = LIB.stat().st_mtime
-    deps = list(CSRC.glob("*")) + [ROOT / "include" / "moe.h", Path(__file__)]
+    deps = [p for p in CSRC.glob("*") if p.suffix != ".cpp"] + [ROOT / "include" / "moe.h", Path(__file__)]
     return any(p.stat().st_mtime > t for p in deps)
 
 
@@ -39,6 +70,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: Path | No
     """Compile every .cu into one shared library; `defines` (e.g. ["MOE_DECODE_STAGES=2"]) and
     `out` build a variant elsewhere."""
     lib = LIB if out is None else Path(out)
+    if out is None:
+        build_ext(force)
     if not force and not defines and out is None and not _stale():
         return LIB
     OUT_DIR.mkdir(exist_ok=True)
