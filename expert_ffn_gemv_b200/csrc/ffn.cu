@@ -21,13 +21,10 @@ using namespace moe;
 
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kGemmSmem = 1024 + 1024 + kStages * kStageBytes;
-constexpr int kGemmThreads = 192;  // warps 0..3 epilogue, 4 TMA producer, 5 MMA
+constexpr int kBK = 64;
+constexpr int kMaxBN = 256;
 constexpr uint64_t kSpin = 2000000000ull;  // about a second
-constexpr int kMaxProb = 4, kMaxMaps = 5;
+constexpr int kMaxProb = 4, kMaxMaps = 9;
 
 // Set by a kernel whose bounded wait ran out; moe_ffn_check reads and clears it.
 __device__ uint32_t g_ffn_err;
@@ -36,7 +33,7 @@ enum { kEpiPlain = 0, kEpiSwiglu = 1, kEpiDswiglu = 2 };
 
 struct GemmProb {
   int m, n, k, segs;       // segs products over k added up (operands a[i], b[i])
-  int tiles_n, tile0;      // tiles along n, first tile of this product in the launch
+  int tiles_m, tiles_n;
   int a[2], b[2];          // tensor map numbers
   int a_mn, b_mn;          // 1: the operand lies along its rows
   void *out;               // plain: [m][ld]
@@ -47,28 +44,88 @@ struct GemmProb {
 
 struct GemmArgs {
   CUtensorMap map[kMaxMaps];
-  GemmProb p[kMaxProb];
-  int n_prob, tiles;
+  GemmProb p[kMaxProb];    // p[0] is dealt out first, then the others as one list
+  int n_prob, bn;          // bn: columns of a tile (swiglu: bn / 2 of g and of u)
   // gated epilogues: n columns of f values
   float *g, *u;                // swiglu: saved unless NULL; dswiglu: read
   __nv_bfloat16 *h, *dg, *du;  // swiglu: h; dswiglu: all three
   int64_t f_ld;
 };
 
+// Threads: EW epilogue warps (TMEM lanes 32 (w % 4) .., 32-column chunks w / 4, w / 4 + EW / 4, ..), a
+// TMA producer warp, an MMA warp.  CG: CTAs of a tile (cta_group); a CTA holds 128 rows of A and
+// bn / CG rows of B per stage.  The gated epilogues of a pair take 16 warps: their arithmetic
+// (some 30 instructions a value, few in flight a warp) took 25 us a tile of 256 x 256 with eight, its
+// 2048-deep product 12 us.
+template <int EPI, int CG>
+struct GemmPlan {
+  static constexpr int EW = EPI != kEpiPlain && CG == 2 ? 16 : 8, kThreads = 32 * (EW + 2);
+  static constexpr int kABytes = 128 * kBK * 2, kBBytes = kMaxBN / CG * kBK * 2, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = CG == 1 ? 4 : EW == 16 ? 5 : 6;
+  static constexpr int kSmem = 1024 + 1024 + kStages * kStageBytes + EW * 4096;
+};
+
 struct GemmTile {
   int p, m0, n0, steps;
 };
-__device__ __forceinline__ GemmTile gemm_tile(const GemmArgs &a, int t) {
-  GemmTile r;
-  r.p = 0;
-  while (r.p + 1 < a.n_prob && t >= a.p[r.p + 1].tile0) ++r.p;
-  const GemmProb &p = a.p[r.p];
-  const int i = t - p.tile0;
-  r.m0 = i / p.tiles_n * kBM;
-  r.n0 = i % p.tiles_n;  // in tiles
-  r.steps = p.segs * ((p.k + kBK - 1) / kBK);
-  return r;
-}
+
+// The tiles of unit c of g (a unit: the CTAs of one tile): p[0]'s tiles c, c + g, ..; then the other
+// products' tiles as one list.  Where p[0] leaves some units a tile short, these take as many of the
+// list's tiles as that tile was worth first, then the list goes round.  Inside a product, bands of
+// eight tile rows, so that the tiles in flight share operands in L2.
+struct GemmWalk {
+  int c, g, n0, rest, r, k0, i, phase;
+  __device__ GemmWalk(const GemmArgs &a, int c_, int g_) : c(c_), g(g_), i(0), phase(0) {
+    n0 = a.p[0].tiles_m * a.p[0].tiles_n;
+    rest = 0;
+    for (int p = 1; p < a.n_prob; ++p) rest += a.p[p].tiles_m * a.p[p].tiles_n;
+    r = n0 % g;
+    k0 = 0;
+    if (rest) {
+      const int s0 = a.p[0].segs * a.p[0].k, s1 = a.p[1].k;
+      k0 = r ? (s0 + s1 / 2) / s1 : 0;
+      if (static_cast<int64_t>(k0) * (g - r) > rest) k0 = rest / (g - r);
+    }
+  }
+  __device__ bool next(const GemmArgs &a, GemmTile &t) {
+    if (phase == 0) {
+      const int j = c + i * g;
+      if (j < n0) {
+        ++i;
+        place(a, 0, j, t);
+        return true;
+      }
+      phase = 1, i = 0;
+    }
+    if (phase == 1) {
+      if (c >= r && i < k0) {
+        const int j = (c - r) + i * (g - r);
+        ++i;
+        return pick(a, j, t);
+      }
+      phase = 2, i = 0;
+    }
+    const int j = k0 * (g - r) + c + i * g;
+    ++i;
+    return j < rest && pick(a, j, t);
+  }
+  __device__ bool pick(const GemmArgs &a, int j, GemmTile &t) {
+    int p = 1;
+    while (p + 1 < a.n_prob && j >= a.p[p].tiles_m * a.p[p].tiles_n) j -= a.p[p].tiles_m * a.p[p].tiles_n, ++p;
+    place(a, p, j, t);
+    return true;
+  }
+  __device__ void place(const GemmArgs &a, int pi, int j, GemmTile &t) {
+    const GemmProb &p = a.p[pi];
+    constexpr int kBand = 8;
+    const int band = j / (kBand * p.tiles_n), in = j - band * kBand * p.tiles_n;
+    const int rows = min(kBand, p.tiles_m - band * kBand);
+    t.p = pi;
+    t.m0 = band * kBand + in % rows;  // in tiles
+    t.n0 = in / rows;
+    t.steps = p.segs * ((p.k + kBK - 1) / kBK);
+  }
+};
 
 // MN-major operand, 128-byte swizzle: blocks of 64 rows x 64 k, each k one 128-byte line of 64
 // rows; 8 k make 1024 bytes (stride offset), the next 64 rows lie 8192 bytes on (leading offset).
@@ -82,223 +139,352 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// ---- the cta_group::2 forms of tc05.cuh's helpers
+template <int CG>
+__device__ __forceinline__ void g_tmem_alloc(uint32_t *dst) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, 512);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void g_tmem_dealloc(uint32_t t) {
+  if constexpr (CG == 1)
+    tmem_dealloc(t, 512);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void g_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 1) {
+    tc_mma(d, a, b, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+// arrives on `bar` of every CTA of the tile
+template <int CG>
+__device__ __forceinline__ void g_commit(uint64_t *bar) {
+  if constexpr (CG == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {  // the same place in CTA 0 of the cluster
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+// a tile of this CTA's operands, counted on the leader's barrier
+template <int CG>
+__device__ __forceinline__ void g_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint32_t leader) {
+  if constexpr (CG == 1)
+    tma_load_2d(dst, map, x, y, bar);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Fast division (2 ulp; 1 / inf = 0): the IEEE one made half of the epilogues' instructions.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-
-// Eight values to or from a row; whole vectors only (f and the strides are multiples of 8).
-__device__ __forceinline__ void put8(__nv_bfloat16 *p, const float *v) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, const float (&v)[4]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
-__device__ __forceinline__ void get8(const __nv_bfloat16 *p, float *v) {
-  const uint4 q = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void put4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ float4 get4(const void *p, int64_t i, int bf16) {
+  if (!bf16) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+  const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+  return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u), __uint_as_float(q.y << 16),
+                     __uint_as_float(q.y & 0xFFFF0000u));
+}
+
+// The epilogue turns chunks of 32 rows x 32 accumulator columns round in shared memory: a lane of the
+// TMEM load holds a row, a lane of the global accesses four columns of a row, so that these are whole
+// sectors of consecutive columns.  16-byte pieces are exchanged (piece ^ row % 8): no bank conflicts.
+__device__ __forceinline__ void turn_in(float *s, const uint32_t (&v)[32], int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int c = 0; c < 8; ++c)
+    reinterpret_cast<uint4 *>(s)[lane * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ float4 turn_out(const float *s, int row, int c) {
+  return reinterpret_cast<const float4 *>(s)[row * 8 + (c ^ (row & 7))];
 }
 
-__device__ __forceinline__ void put8(float *p, const float *v) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void get8(const float *p, float *v) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_constant__ GemmArgs a) {
+template <int EPI, int CG>
+__global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(const __grid_constant__ GemmArgs a) {
+  using PL = GemmPlan<EPI, CG>;
+  constexpr int NS = PL::kStages, EW = PL::EW;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + kStages, *acc_full = empty + kStages,
-           *acc_empty = acc_full + 2;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + NS, *acc_full = empty + NS, *acc_empty = acc_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 516);
   unsigned char *stages = smem + 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int bn = a.bn, bl = bn / CG;  // columns of a tile, B rows of a CTA
   uint32_t *err = &g_ffn_err;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 128);
+      mbar_init(&acc_empty[b], EW * CG);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 0) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
+  if (warp == 0) g_tmem_alloc<CG>(tmem_slot);
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  GemmWalk walk(a, unit, units);
+  GemmTile tl;
 
-  if (warp == 4) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-        const GemmTile tl = gemm_tile(a, t);
-        const GemmProb &p = a.p[tl.p];
-        const int per = tl.steps / p.segs;
-        for (int s = 0; s < tl.steps; ++s, ++it) {
-          const int st = it % kStages;
-          if (it >= kStages && !(ok = pf_wait(&empty[st], ((it / kStages) - 1) & 1u, kSpin, abort_flag, err))) break;
-          const int seg = s >= per, k0 = (s - seg * per) * kBK;
-          unsigned char *sa = stages + st * kStageBytes, *sb = sa + kABytes;
-          mbar_arrive_expect_tx(&full[st], kStageBytes);
-          const CUtensorMap *ma = &a.map[p.a[seg]];
-          if (p.a_mn)
-            for (int i = 0; i < kBM / 64; ++i) tma_load_2d(sa + i * 8192, ma, tl.m0 + 64 * i, k0, &full[st]);
-          else
-            tma_load_2d(sa, ma, k0, tl.m0, &full[st]);
-          if (EPI == kEpiSwiglu) {  // 128 rows of Wg, then the same rows of Wu
-            tma_load_2d(sb, &a.map[p.b[0]], k0, tl.n0 * 128, &full[st]);
-            tma_load_2d(sb + kBBytes / 2, &a.map[p.b[1]], k0, tl.n0 * 128, &full[st]);
-          } else {
-            const CUtensorMap *mb = &a.map[p.b[seg]];
-            if (p.b_mn) {
-              for (int i = 0; i < kBN / 64; ++i) tma_load_2d(sb + i * 8192, mb, tl.n0 * kBN + 64 * i, k0, &full[st]);
-            } else {
-              tma_load_2d(sb, mb, k0, tl.n0 * kBN, &full[st]);
-              tma_load_2d(sb + kBBytes / 2, mb, k0, tl.n0 * kBN + 128, &full[st]);
-            }
-          }
-        }
+  if (warp == EW) {
+    // ---------------- producer: this CTA's rows of both operands.  Lane l issues the step's copy l (the
+    // one or two boxes of A, then those of B), with its map and coordinates worked out once a tile: one
+    // lane that issued them all and looked them up spent 880 clocks a step on it, the MMAs take 512.
+    uint32_t it = 0;
+    bool ok = true;
+    const uint32_t tx = CG * (PL::kABytes + bl * kBK * 2);
+    while (ok && walk.next(a, tl)) {
+      const GemmProb &p = a.p[tl.p];
+      const int per = tl.steps / p.segs, m0 = (tl.m0 * CG + rank) * 128, na = p.a_mn ? 2 : 1;
+      const bool is_a = lane < na, mine = lane < na + bl / 64, mn = is_a ? p.a_mn : p.b_mn;
+      const int box = is_a ? lane : lane - na;
+      const uint32_t off = is_a ? box * 8192 : PL::kABytes + box * 8192;
+      int row = is_a ? m0 + 64 * box : rank * bl + 64 * box, m_first = is_a ? p.a[0] : p.b[0], m_then = is_a ? p.a[1] : p.b[1];
+      if (!is_a && EPI == kEpiSwiglu) {
+        // the first half of the tile's B rows are Wg's, the second half the same rows of Wu
+        const int half = bn / 2, up = row >= half;
+        m_first = up ? m_then : m_first;
+        row = tl.n0 * half + row - up * half;
+      } else if (!is_a) {
+        row += tl.n0 * bn;
       }
-      // leave only once every copy has landed
-      for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-        mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1u, kDrainLimit);
+      const CUtensorMap *map = &a.map[m_first];
+      const CUtensorMap *then = &a.map[m_then];
+      int k = 0;
+      for (int s = 0; s < tl.steps; ++s, ++it) {
+        const int st = it % NS;
+        const bool got = it < NS || pf_wait(&empty[st], ((it / NS) - 1) & 1u, kSpin, abort_flag, err);
+        if (!(ok = __all_sync(0xffffffffu, got))) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[st], tx);
+        __syncwarp();
+        if (s == per) map = then, k = 0;
+        if (mine)
+          g_load<CG>(stages + st * PL::kStageBytes + off, map, mn ? row : k, mn ? k : row, &full[st],
+                     CG == 2 ? leader_addr(&full[st]) : 0);
+        k += kBK;
+      }
     }
-  } else if (warp == 5) {
-    if (lane == 0) {
+    __syncwarp();
+    // leave only once every copy has landed (the leader's barriers count both CTAs' copies) and every
+    // stage's commit has arrived
+    if (lane == 0)
+      for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) {
+        if (rank == 0) mbar_wait_bounded(&full[k % NS], (k / NS) & 1u, kDrainLimit);
+        if (ok) mbar_wait_bounded(&empty[k % NS], (k / NS) & 1u, kDrainLimit);
+      }
+  } else if (warp == EW + 1) {
+    // ---------------- MMA issue (one thread of the leader)
+    if (lane == 0 && rank == 0) {
       uint32_t it = 0, n = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n) {
-        const GemmTile tl = gemm_tile(a, t);
+      for (; ok && walk.next(a, tl); ++n) {
         const GemmProb &p = a.p[tl.p];
         const int b = n & 1;
         if (n >= 2 && !(ok = pf_wait(&acc_empty[b], ((n >> 1) - 1) & 1u, kSpin, abort_flag, err))) break;
         tc_fence_after();
-        const uint32_t idesc = idesc_bf16(kBN) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = (idesc_bf16(bn) & 0x00FFFFFFu) | (static_cast<uint32_t>(128 * CG >> 4) << 24) |
+                               (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
         const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint32_t sa = smem_u32(stages), sb = sa + PL::kABytes;
+        const uint64_t ad0 = p.a_mn ? mn_desc(sa) : sw128_desc(sa), bd0 = p.b_mn ? mn_desc(sb) : sw128_desc(sb);
+        const uint32_t acc = tmem + b * kMaxBN;
         for (int s = 0; s < tl.steps; ++s, ++it) {
-          const int st = it % kStages;
-          if (!(ok = pf_wait(&full[st], (it / kStages) & 1u, kSpin, abort_flag, err))) break;
+          const int st = it % NS;
+          if (!(ok = pf_wait(&full[st], (it / NS) & 1u, kSpin, abort_flag, err))) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(stages + st * kStageBytes), sb = sa + kABytes;
-          const uint64_t ad = p.a_mn ? mn_desc(sa) : sw128_desc(sa), bd = p.b_mn ? mn_desc(sb) : sw128_desc(sb);
+          const uint64_t ad = ad0 + (st * PL::kStageBytes >> 4), bd = bd0 + (st * PL::kStageBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma(tmem + b * kBN, ad + kk * a_step, bd + kk * b_step, idesc, s > 0 || kk > 0);
-          tc_commit(&empty[st]);
+            g_mma<CG>(acc, ad + kk * a_step, bd + kk * b_step, idesc, s > 0 || kk > 0);
+          g_commit<CG>(&empty[st]);
         }
-        if (ok) tc_commit(&acc_full[b]);
+        if (ok) g_commit<CG>(&acc_full[b]);
       }
-      if (it > 0) mbar_wait_bounded(&empty[(it - 1) % kStages], ((it - 1) / kStages) & 1u, kDrainLimit);
+      if (it > 0) mbar_wait_bounded(&empty[(it - 1) % NS], ((it - 1) / NS) & 1u, kDrainLimit);
     }
   } else {
+    // ---------------- epilogue
+    float *scratch = reinterpret_cast<float *>(stages + NS * PL::kStageBytes + warp * 4096);
+    const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     uint32_t n = 0;
-    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
-      const GemmTile tl = gemm_tile(a, t);
-      const GemmProb &p = a.p[tl.p];
-      const int b = n & 1;
-      if (!pf_wait(&acc_full[b], (n >> 1) & 1u, kSpin, abort_flag, err)) break;
+    while (walk.next(a, tl)) {
+      const int b = n & 1, rows = a.p[tl.p].m, cols = a.p[tl.p].n;
+      const int row0 = (tl.m0 * CG + rank) * 128 + 32 * (warp & 3);
+      const uint32_t acc = tmem + b * kMaxBN + quad;
+      // dswiglu: the first g and u are on their way while the accumulators are waited for
+      float4 gq[4], uq[4];
+      const int c = lane & 7;
+      auto fetch = [&](int h) {  // rows 16 (h % 2) .. of this warp's column chunk h / 2
+        const int col = tl.n0 * bn + 32 * (warp >> 2) + 8 * EW * (h >> 1) + 4 * c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + 16 * (h & 1) + 4 * i + (lane >> 3);
+          if (row < rows && col < cols) {
+            gq[i] = *reinterpret_cast<const float4 *>(a.g + row * a.f_ld + col);
+            uq[i] = *reinterpret_cast<const float4 *>(a.u + row * a.f_ld + col);
+          }
+        }
+      };
+      if (EPI == kEpiDswiglu) fetch(0);
+      if (!__all_sync(0xffffffffu, pf_wait(&acc_full[b], (n >> 1) & 1u, kSpin, abort_flag, err))) break;
+      ++n;
       tc_fence_after();
-      const int row = tl.m0 + 32 * warp + lane;
-      const uint32_t acc = tmem + b * kBN + (static_cast<uint32_t>(32 * warp) << 16);
       if (EPI == kEpiSwiglu) {
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t g[32], u[32];
-          tmem_ld32_nowait(acc + c0, g);
-          tmem_ld32_nowait(acc + 128 + c0, u);
+        const int half = bn / 2, cc = lane & 3;
+        float *gs = a.g, *us = a.u;
+        const int64_t ld = a.f_ld;
+        for (int c0 = 16 * (warp >> 2); c0 < half; c0 += 4 * EW) {
+          uint32_t v[32];
+          tmem_ld16_nowait(acc + c0, v);
+          tmem_ld16_nowait(acc + half + c0, v + 16);
           tmem_wait_ld();
-          const int col = tl.n0 * 128 + c0;
+          __syncwarp();
+          turn_in(scratch, v, lane);
+          __syncwarp();
+          const int col = tl.n0 * half + c0 + 4 * cc;
+          if (col < cols) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (row >= p.m || col + i >= p.n) continue;
-            const int64_t at = static_cast<int64_t>(row) * a.f_ld + col + i;
-            float gv[8], uv[8], hv[8];
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2), row = row0 + r;
+              const float4 gf = turn_out(scratch, r, cc), uf = turn_out(scratch, r, 4 + cc);
+              if (row >= rows) continue;
+              const int64_t at = row * ld + col;
+              const float gv[4] = {gf.x, gf.y, gf.z, gf.w}, uv[4] = {uf.x, uf.y, uf.z, uf.w};
+              float hv[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              gv[k] = __uint_as_float(g[i + k]);
-              uv[k] = __uint_as_float(u[i + k]);
-              hv[k] = gv[k] * sigmoid_f(gv[k]) * uv[k];
-            }
-            put8(a.h + at, hv);
-            if (a.g) {
-              put8(a.g + at, gv);
-              put8(a.u + at, uv);
+              for (int k = 0; k < 4; ++k) hv[k] = gv[k] * sigmoid_f(gv[k]) * uv[k];
+              put4(a.h + at, hv);
+              if (gs) {
+                put4(gs + at, gv);
+                put4(us + at, uv);
+              }
             }
           }
         }
       } else {
-        for (int c0 = 0; c0 < kBN; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32_nowait(acc + c0, v);
-          tmem_wait_ld();
-          const int col = tl.n0 * kBN + c0;
+        const void *add = a.p[tl.p].add;
+        void *out = a.p[tl.p].out;
+        const int64_t ld = a.p[tl.p].ld, add_ld = a.p[tl.p].add_ld;
+        const int out_bf16 = a.p[tl.p].out_bf16, add_bf16 = a.p[tl.p].add_bf16;
+        auto half = [&](int h) {
+          const int col = tl.n0 * bn + 32 * (warp >> 2) + 8 * EW * (h >> 1) + 4 * c;
+          if (col >= cols) return;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (row >= p.m || col + i >= p.n) continue;
-            float d[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = __uint_as_float(v[i + k]);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 16 * (h & 1) + 4 * i + (lane >> 3), row = row0 + r;
+            const float4 q = turn_out(scratch, r, c);
+            if (row >= rows) continue;
+            float d[4] = {q.x, q.y, q.z, q.w};
             if (EPI == kEpiDswiglu) {
-              const int64_t at = static_cast<int64_t>(row) * a.f_ld + col + i;
-              float gv[8], uv[8], hv[8], dg[8], du[8];
-              get8(a.g + at, gv);
-              get8(a.u + at, uv);
+              const int64_t at = row * a.f_ld + col;
+              const float gv[4] = {gq[i].x, gq[i].y, gq[i].z, gq[i].w}, uv[4] = {uq[i].x, uq[i].y, uq[i].z, uq[i].w};
+              float hv[4], dg[4], du[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < 4; ++k) {
                 const float sg = sigmoid_f(gv[k]), sl = gv[k] * sg;
                 hv[k] = sl * uv[k];
                 du[k] = d[k] * sl;
-                dg[k] = d[k] * uv[k] * (sg * (1.f + gv[k] * (1.f - sg)));
+                dg[k] = d[k] * uv[k] * fmaf(sl, 1.f - sg, sg);
               }
-              put8(a.h + at, hv);
-              put8(a.dg + at, dg);
-              put8(a.du + at, du);
+              put4(a.h + at, hv);
+              put4(a.dg + at, dg);
+              put4(a.du + at, du);
             } else {
-              if (p.add) {
-                const int64_t at = static_cast<int64_t>(row) * p.add_ld + col + i;
-                float e[8];
-                if (p.add_bf16)
-                  get8(static_cast<const __nv_bfloat16 *>(p.add) + at, e);
-                else
-                  get8(static_cast<const float *>(p.add) + at, e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] += e[k];
+              if (add) {
+                const float4 e = get4(add, row * add_ld + col, add_bf16);
+                d[0] += e.x; d[1] += e.y; d[2] += e.z; d[3] += e.w;
               }
-              const int64_t at = static_cast<int64_t>(row) * p.ld + col + i;
-              if (p.out_bf16)
-                put8(static_cast<__nv_bfloat16 *>(p.out) + at, d);
+              if (out_bf16)
+                put4(static_cast<__nv_bfloat16 *>(out) + row * ld + col, d);
               else
-                put8(static_cast<float *>(p.out) + at, d);
+                put4(static_cast<float *>(out) + row * ld + col, d);
             }
           }
+        };
+        for (int c0 = 32 * (warp >> 2), h = 0; c0 < bn; c0 += 8 * EW, h += 2) {
+          if (EPI == kEpiDswiglu && h) fetch(h);
+          uint32_t v[32];
+          tmem_ld32_nowait(acc + c0, v);
+          tmem_wait_ld();
+          __syncwarp();
+          turn_in(scratch, v, lane);
+          __syncwarp();
+          half(h);
+          if (EPI == kEpiDswiglu) fetch(h + 1);
+          half(h + 1);
         }
       }
       tc_fence_before();
-      mbar_arrive(&acc_empty[b]);
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(&acc_empty[b])) : "memory");
+        else
+          mbar_arrive(&acc_empty[b]);
+      }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  // a CTA's shared memory is read by the pair's MMAs and its barriers are arrived on by the other CTA
+  if (CG == 2) cluster_sync();
+  if (warp == 0) g_tmem_dealloc<CG>(tmem);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -420,33 +606,64 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Once per device, with it current: the encoder's address and the kernels' shared-memory limit.
-cudaError_t ffn_setup(EncodeFn *out) {
+template <int EPI>
+cudaError_t configure_gemm() {
+  cudaError_t e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmPlan<EPI, 1>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmPlan<EPI, 2>::kSmem);
+  return e;
+}
+
+template <int EPI>
+void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int grid, cudaStream_t st) {
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(GemmPlan<EPI, 2>::kThreads);
+  cfg.dynamicSmemBytes = GemmPlan<EPI, 2>::kSmem;
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+}
+
+struct FfnDevice {
+  EncodeFn encode;
+  int nsm, pairs;  // CTA pairs the device holds at once
+};
+
+// Once per device, with it current: the encoder's address, the kernels' shared-memory limit, sizes.
+cudaError_t ffn_setup(FfnDevice *out) {
   constexpr int kMaxDevices = 64;
   static std::mutex mutex;
-  static EncodeFn encode = nullptr;
-  static bool ready[kMaxDevices] = {};
+  static FfnDevice known[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices) return cudaErrorNotSupported;
   std::lock_guard<std::mutex> lock(mutex);
-  if (!encode) {
+  FfnDevice &k = known[dev];
+  if (!k.encode) {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
     if (e != cudaSuccess) return e;
     if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    encode = reinterpret_cast<EncodeFn>(fn);
+    e = current_sm_count(&k.nsm);
+    if (e == cudaSuccess) e = configure_gemm<kEpiPlain>();
+    if (e == cudaSuccess) e = configure_gemm<kEpiSwiglu>();
+    if (e == cudaSuccess) e = configure_gemm<kEpiDswiglu>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    pair_config<kEpiPlain>(cfg, at, 2, nullptr);
+    e = cudaOccupancyMaxActiveClusters(&k.pairs, k_ffn_gemm<kEpiPlain, 2>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (k.pairs > k.nsm / 2) k.pairs = k.nsm / 2;
+    k.encode = reinterpret_cast<EncodeFn>(fn);
   }
-  if (!ready[dev]) {
-    const void *ks[] = {(const void *)k_ffn_gemm<kEpiPlain>, (const void *)k_ffn_gemm<kEpiSwiglu>,
-                        (const void *)k_ffn_gemm<kEpiDswiglu>};
-    for (const void *k : ks)
-      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem)) != cudaSuccess) return e;
-    ready[dev] = true;
-  }
-  *out = encode;
+  *out = k;
   return cudaSuccess;
 }
 
@@ -470,19 +687,57 @@ struct Maps {
   }
 };
 
-GemmProb &add_prob(GemmArgs &a, int m, int n, int k, int tile_n) {
+GemmProb &add_prob(GemmArgs &a, int m, int n, int k) {
   GemmProb &p = a.p[a.n_prob++];
   p.m = m, p.n = n, p.k = k, p.segs = 1;
-  p.tiles_n = (n + tile_n - 1) / tile_n;
-  p.tile0 = a.tiles;
-  a.tiles += (m + kBM - 1) / kBM * p.tiles_n;
   return p;
 }
 
+// Sizes the tiles and launches.  A unit is one CTA on tiles of 128 x bn or a pair of CTAs on tiles of
+// 256 x 256, which read half as many operand bytes for their products; the rule takes what fills the
+// device in the least time, by the clocks of a 64-deep step of each tile (kStep).
 template <int EPI>
-cudaError_t launch_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
-  k_ffn_gemm<EPI><<<a.tiles < nsm ? a.tiles : nsm, kGemmThreads, kGemmSmem, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
+  struct Form {
+    int cg, bn, step;
+  };
+  constexpr Form forms[] = {{2, 256, 520}, {1, 256, 640}, {1, 128, 400}, {1, 64, 320}};
+  double best = 0;
+  Form f{};
+  for (const Form &c : forms) {
+    if (EPI == kEpiSwiglu && c.bn == 64) continue;  // 64 rows each of two matrices at least
+    const int cols = EPI == kEpiSwiglu ? c.bn / 2 : c.bn, units = c.cg == 2 ? dev.pairs : dev.nsm;
+    if (units < 1) continue;
+    double steps = 0, longest = 0;  // of all tiles and of the longest
+    for (int i = 0; i < a.n_prob; ++i) {
+      const GemmProb &p = a.p[i];
+      const double len = p.segs * ((p.k + kBK - 1) / kBK) + 4;  // 4: filling and draining
+      const double tiles = static_cast<double>((p.m + 128 * c.cg - 1) / (128 * c.cg)) * ((p.n + cols - 1) / cols);
+      // alone, whole rounds of tiles; among others, what is left over is filled up
+      steps += a.n_prob == 1 ? len * units * static_cast<int>((tiles + units - 1) / units) : len * tiles;
+      longest = longest > len ? longest : len;
+    }
+    const double t = (steps / units > longest ? steps / units : longest) * c.step;
+    if (!f.cg || t < best) best = t, f = c;
+  }
+  a.bn = f.bn;
+  const int cols = EPI == kEpiSwiglu ? f.bn / 2 : f.bn;
+  int tiles = 0;
+  for (int i = 0; i < a.n_prob; ++i) {
+    GemmProb &p = a.p[i];
+    p.tiles_m = (p.m + 128 * f.cg - 1) / (128 * f.cg);
+    p.tiles_n = (p.n + cols - 1) / cols;
+    tiles += p.tiles_m * p.tiles_n;
+  }
+  const int units = f.cg == 2 ? dev.pairs : dev.nsm, grid = (tiles < units ? tiles : units) * f.cg;
+  if (f.cg == 1) {
+    k_ffn_gemm<EPI, 1><<<grid, GemmPlan<EPI, 1>::kThreads, GemmPlan<EPI, 1>::kSmem, st>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  pair_config<EPI>(cfg, at, grid, st);
+  return cudaLaunchKernelEx(&cfg, k_ffn_gemm<EPI, 2>, a);
 }
 
 constexpr int kMaxDim = 65536;
@@ -536,35 +791,34 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     e = cudaGetLastError();
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
-  EncodeFn encode = nullptr;
-  int nsm = 0;
-  if ((e = ffn_setup(&encode)) != cudaSuccess || (e = current_sm_count(&nsm)) != cudaSuccess) {
+  FfnDevice dev{};
+  if ((e = ffn_setup(&dev)) != cudaSuccess) {
     cudaGetLastError();
     return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
   }
   GemmArgs a{};
   {
-    Maps m{encode, a};
-    GemmProb &q = add_prob(a, n, f, d, 128);
-    q.a[0] = m.add(p->x, n, d, p->x_stride, kBM);
-    q.b[0] = m.add(p->w_gate, f, d, d, 128);
-    q.b[1] = m.add(p->w_up, f, d, d, 128);
+    Maps m{dev.encode, a};
+    GemmProb &q = add_prob(a, n, f, d);
+    q.a[0] = m.add(p->x, n, d, p->x_stride, 128);
+    q.b[0] = m.add(p->w_gate, f, d, d, 64);
+    q.b[1] = m.add(p->w_up, f, d, d, 64);
     a.h = h, a.g = static_cast<float *>(p->save_gate), a.u = static_cast<float *>(p->save_up);
     a.f_ld = f;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
-  if ((e = launch_gemm<kEpiSwiglu>(a, nsm, st)) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
   GemmArgs b{};
   {
-    Maps m{encode, b};
-    GemmProb &q = add_prob(b, n, d, f, kBN);
-    q.a[0] = m.add(h, n, f, f, kBM);
-    q.b[0] = m.add(p->w_down, d, f, f, 128);
+    Maps m{dev.encode, b};
+    GemmProb &q = add_prob(b, n, d, f);
+    q.a[0] = m.add(h, n, f, f, 128);
+    q.b[0] = m.add(p->w_down, d, f, f, 64);
     q.out = p->y, q.ld = p->y_stride, q.out_bf16 = p->y_dtype == MOE_BF16;
     q.add = p->add, q.add_ld = p->add_stride, q.add_bf16 = p->add_dtype == MOE_BF16;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
-  e = launch_gemm<kEpiPlain>(b, nsm, st);
+  e = launch_gemm<kEpiPlain>(b, dev, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -579,10 +833,9 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
       p->workspace_bytes < moe_ffn_workspace(n, d, f, 1))
     return MOE_ERR_INVALID_ARGUMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  EncodeFn encode = nullptr;
-  int nsm = 0;
+  FfnDevice dev{};
   cudaError_t e;
-  if ((e = ffn_setup(&encode)) != cudaSuccess || (e = current_sm_count(&nsm)) != cudaSuccess) {
+  if ((e = ffn_setup(&dev)) != cudaSuccess) {
     cudaGetLastError();
     return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
   }
@@ -590,47 +843,42 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
   __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(p->workspace), *dg = h + nf, *du = dg + nf;
   {
     GemmArgs a{};
-    Maps m{encode, a};
-    GemmProb &q = add_prob(a, n, f, d, kBN);
-    q.a[0] = m.add(p->dy, n, d, p->dy_stride, kBM);
+    Maps m{dev.encode, a};
+    GemmProb &q = add_prob(a, n, f, d);
+    q.a[0] = m.add(p->dy, n, d, p->dy_stride, 128);
     q.b[0] = m.add(p->w_down, d, f, f, kBK), q.b_mn = 1;
     a.g = static_cast<float *>(const_cast<void *>(p->save_gate)), a.u = static_cast<float *>(const_cast<void *>(p->save_up));
     a.h = h, a.dg = dg, a.du = du, a.f_ld = f;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-    if ((e = launch_gemm<kEpiDswiglu>(a, nsm, st)) != cudaSuccess) return MOE_ERR_CUDA;
+    if ((e = launch_gemm<kEpiDswiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
   }
+  // everything else in one launch: dx (its tiles run over both matrices), then the weights' gradients
+  GemmArgs a{};
+  Maps m{dev.encode, a};
   if (p->dx) {
-    GemmArgs a{};
-    Maps m{encode, a};
-    GemmProb &q = add_prob(a, n, d, f, kBN);
+    GemmProb &q = add_prob(a, n, d, f);
     q.segs = 2;
-    q.a[0] = m.add(dg, n, f, f, kBM), q.a[1] = m.add(du, n, f, f, kBM);
+    q.a[0] = m.add(dg, n, f, f, 128), q.a[1] = m.add(du, n, f, f, 128);
     q.b[0] = m.add(p->w_gate, f, d, d, kBK), q.b[1] = m.add(p->w_up, f, d, d, kBK), q.b_mn = 1;
     q.out = p->dx, q.ld = p->dx_stride, q.out_bf16 = 1;
-    if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-    if ((e = launch_gemm<kEpiPlain>(a, nsm, st)) != cudaSuccess) return MOE_ERR_CUDA;
   }
-  if (p->dw_gate || p->dw_down) {
-    GemmArgs a{};
-    Maps m{encode, a};
-    const int mh = p->dw_down ? m.add(h, n, f, f, kBK) : 0, mdy = p->dw_down ? m.add(p->dy, n, d, p->dy_stride, kBK) : 0;
-    if (p->dw_gate) {
-      const int mx = m.add(p->x, n, d, p->x_stride, kBK);
-      for (int i = 0; i < 2; ++i) {
-        GemmProb &q = add_prob(a, f, d, n, kBN);
-        q.a[0] = m.add(i ? du : dg, n, f, f, kBK), q.b[0] = mx, q.a_mn = q.b_mn = 1;
-        q.out = i ? p->dw_up : p->dw_gate, q.ld = d, q.out_bf16 = 1;
-      }
+  if (p->dw_gate) {
+    const int mx = m.add(p->x, n, d, p->x_stride, kBK);
+    const int rows[2] = {m.add(dg, n, f, f, kBK), m.add(du, n, f, f, kBK)};
+    for (int i = 0; i < 2; ++i) {
+      GemmProb &q = add_prob(a, f, d, n);
+      q.a[0] = rows[i], q.b[0] = mx, q.a_mn = q.b_mn = 1;
+      q.out = i ? p->dw_up : p->dw_gate, q.ld = d, q.out_bf16 = 1;
     }
-    if (p->dw_down) {
-      GemmProb &q = add_prob(a, d, f, n, kBN);
-      q.a[0] = mdy, q.b[0] = mh, q.a_mn = q.b_mn = 1;
-      q.out = p->dw_down, q.ld = f, q.out_bf16 = 1;
-    }
-    if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-    if ((e = launch_gemm<kEpiPlain>(a, nsm, st)) != cudaSuccess) return MOE_ERR_CUDA;
   }
-  return MOE_OK;
+  if (p->dw_down) {
+    GemmProb &q = add_prob(a, d, f, n);
+    q.a[0] = m.add(p->dy, n, d, p->dy_stride, kBK), q.b[0] = m.add(h, n, f, f, kBK), q.a_mn = q.b_mn = 1;
+    q.out = p->dw_down, q.ld = f, q.out_bf16 = 1;
+  }
+  if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
+  e = launch_gemm<kEpiPlain>(a, dev, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status moe_ffn_check(void) {
