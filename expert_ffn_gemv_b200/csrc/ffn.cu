@@ -34,6 +34,8 @@ enum { kEpiPlain = 0, kEpiSwiglu = 1, kEpiDswiglu = 2 };
 struct GemmProb {
   int m, n, k, segs;       // segs products over k added up (operands a[i], b[i])
   int tiles_m, tiles_n;
+  int splits;              // the k range in so many pieces, piece s to out + s split_ld (fp32)
+  int64_t split_ld;
   int a[2], b[2];          // tensor map numbers
   int a_mn, b_mn;          // 1: the operand lies along its rows
   void *out;               // plain: [m][ld]
@@ -52,21 +54,17 @@ struct GemmArgs {
   int64_t f_ld;
 };
 
-// Threads: EW epilogue warps (TMEM lanes 32 (w % 4) .., 32-column chunks w / 4, w / 4 + EW / 4, ..), a
-// TMA producer warp, an MMA warp.  CG: CTAs of a tile (cta_group); a CTA holds 128 rows of A and
-// bn / CG rows of B per stage.  The gated epilogues of a pair take 16 warps: their arithmetic
-// (some 30 instructions a value, few in flight a warp) took 25 us a tile of 256 x 256 with eight, its
-// 2048-deep product 12 us.
-template <int EPI, int CG>
-struct GemmPlan {
-  static constexpr int EW = EPI != kEpiPlain && CG == 2 ? 16 : 8, kThreads = 32 * (EW + 2);
-  static constexpr int kABytes = 128 * kBK * 2, kBBytes = kMaxBN / CG * kBK * 2, kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = CG == 1 ? 4 : EW == 16 ? 5 : 6;
-  static constexpr int kSmem = 1024 + 1024 + kStages * kStageBytes + EW * 4096;
-};
+// Threads: sixteen epilogue warps (TMEM lanes 32 (w % 4) .., 32-column chunks w / 4, w / 4 + 4), a TMA
+// producer warp, an MMA warp.  A CTA holds 128 rows of A and up to 128 rows of B per stage: tiles of
+// 128 x 128 for one CTA, of 256 x 256 for a pair (cta_group::2), whose CTAs share their halves of B.
+// With eight epilogue warps the arithmetic of the gated ones (some 30 instructions a value) took 25 us
+// a tile of 256 x 256, its 2048-deep product 12 us, and the last tile's plain one 4.3 us.
+constexpr int kEpiWarps = 16, kGemmThreads = 32 * (kEpiWarps + 2);
+constexpr int kABytes = 128 * kBK * 2, kBBytes = 128 * kBK * 2, kStageBytes = kABytes + kBBytes, kStages = 5;
+constexpr int kGemmSmem = 1024 + 1024 + kStages * kStageBytes + kEpiWarps * 4096;
 
 struct GemmTile {
-  int p, m0, n0, steps;
+  int p, m0, n0, s0, steps, split;  // k steps s0 .. s0 + steps - 1
 };
 
 // The tiles of unit c of g (a unit: the CTAs of one tile): p[0]'s tiles c, c + g, ..; then the other
@@ -75,14 +73,17 @@ struct GemmTile {
 // eight tile rows, so that the tiles in flight share operands in L2.
 struct GemmWalk {
   int c, g, n0, rest, r, k0, i, phase;
-  __device__ GemmWalk(const GemmArgs &a, int c_, int g_) : c(c_), g(g_), i(0), phase(0) {
-    n0 = a.p[0].tiles_m * a.p[0].tiles_n;
+  int cur;  // product whose numbers are held here: a tile is placed without loads or integer divisions
+  int tiles_m, tiles_n, steps, splits;
+  float inv_tiles, inv_band;
+  __device__ GemmWalk(const GemmArgs &a, int c_, int g_) : c(c_), g(g_), i(0), phase(0), cur(-1) {
+    n0 = a.p[0].tiles_m * a.p[0].tiles_n * a.p[0].splits;
     rest = 0;
     for (int p = 1; p < a.n_prob; ++p) rest += a.p[p].tiles_m * a.p[p].tiles_n;
     r = n0 % g;
     k0 = 0;
     if (rest) {
-      const int s0 = a.p[0].segs * a.p[0].k, s1 = a.p[1].k;
+      const int s0 = a.p[0].segs * a.p[0].k / a.p[0].splits, s1 = a.p[1].k;
       k0 = r ? (s0 + s1 / 2) / s1 : 0;
       if (static_cast<int64_t>(k0) * (g - r) > rest) k0 = rest / (g - r);
     }
@@ -101,29 +102,46 @@ struct GemmWalk {
       if (c >= r && i < k0) {
         const int j = (c - r) + i * (g - r);
         ++i;
-        return pick(a, j, t);
+        pick(a, j, t);
+        return true;
       }
       phase = 2, i = 0;
     }
     const int j = k0 * (g - r) + c + i * g;
     ++i;
-    return j < rest && pick(a, j, t);
+    if (j >= rest) return false;
+    pick(a, j, t);
+    return true;
   }
-  __device__ bool pick(const GemmArgs &a, int j, GemmTile &t) {
+  __device__ void pick(const GemmArgs &a, int j, GemmTile &t) {
     int p = 1;
     while (p + 1 < a.n_prob && j >= a.p[p].tiles_m * a.p[p].tiles_n) j -= a.p[p].tiles_m * a.p[p].tiles_n, ++p;
     place(a, p, j, t);
-    return true;
+  }
+  // j / d for j, d < 2^22: the float quotient is off by less than one
+  static __device__ int div(int j, int d, float inv) {
+    int q = static_cast<int>(static_cast<float>(j) * inv);
+    q += (q + 1) * d <= j;
+    q -= q * d > j;
+    return q;
   }
   __device__ void place(const GemmArgs &a, int pi, int j, GemmTile &t) {
-    const GemmProb &p = a.p[pi];
     constexpr int kBand = 8;
-    const int band = j / (kBand * p.tiles_n), in = j - band * kBand * p.tiles_n;
-    const int rows = min(kBand, p.tiles_m - band * kBand);
+    if (pi != cur) {
+      const GemmProb &p = a.p[pi];
+      cur = pi, tiles_m = p.tiles_m, tiles_n = p.tiles_n, splits = p.splits;
+      steps = p.segs * ((p.k + kBK - 1) / kBK);
+      inv_tiles = 1.f / (tiles_m * tiles_n), inv_band = 1.f / (kBand * tiles_n);
+    }
     t.p = pi;
-    t.m0 = band * kBand + in % rows;  // in tiles
-    t.n0 = in / rows;
-    t.steps = p.segs * ((p.k + kBK - 1) / kBK);
+    t.split = splits > 1 ? div(j, tiles_m * tiles_n, inv_tiles) : 0;
+    j -= t.split * tiles_m * tiles_n;
+    t.s0 = splits > 1 ? steps * t.split / splits : 0;
+    t.steps = (splits > 1 ? steps * (t.split + 1) / splits : steps) - t.s0;
+    const int band = div(j, kBand * tiles_n, inv_band), in = j - band * kBand * tiles_n;
+    const int rows = min(kBand, tiles_m - band * kBand);
+    t.n0 = rows == kBand ? in / kBand : in / rows;
+    t.m0 = band * kBand + in - t.n0 * rows;
   }
 };
 
@@ -236,19 +254,43 @@ __device__ __forceinline__ float4 turn_out(const float *s, int row, int c) {
   return reinterpret_cast<const float4 *>(s)[row * 8 + (c ^ (row & 7))];
 }
 
-__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t *r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 32 rows x 32 columns of bf16 results, a row a lane, to global memory: turned in 2 KB, then a lane
+// stores eight columns (16 bytes), four lanes a row.
+__device__ __forceinline__ void store_bf16(float *scratch, const uint32_t (&v)[16], int lane, __nv_bfloat16 *out, int64_t ld,
+                                           int row0, int rows, int col0, int cols) {
+  uint4 *s = reinterpret_cast<uint4 *>(scratch);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    s[lane * 4 + (c ^ ((lane >> 1) & 3))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  const int r0 = lane >> 2, c = lane & 3, col = col0 + 8 * c;
+  uint4 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = s[(r0 + 8 * i) * 4 + (c ^ (((r0 + 8 * i) >> 1) & 3))];
+  __nv_bfloat16 *p = out + (row0 + r0) * ld + col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col < cols && row0 + r0 + 8 * i < rows) *reinterpret_cast<uint4 *>(p + 8 * i * ld) = q[i];
+}
+// The same for fp32: 4 KB, four columns a lane, eight lanes a row.
+__device__ __forceinline__ void store_f32(float *scratch, const uint32_t (&v)[32], int lane, float *out, int64_t ld, int row0,
+                                          int rows, int col0, int cols) {
+  __syncwarp();
+  turn_in(scratch, v, lane);
+  __syncwarp();
+  const int r0 = lane >> 3, c = lane & 7, col = col0 + 4 * c;
+  float *p = out + (row0 + r0) * ld + col;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 q = turn_out(scratch, r0 + 4 * i, c);
+    if (col < cols && row0 + r0 + 4 * i < rows) *reinterpret_cast<float4 *>(p + 4 * i * ld) = q;
+  }
 }
 
 template <int EPI, int CG>
-__global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(const __grid_constant__ GemmArgs a) {
-  using PL = GemmPlan<EPI, CG>;
-  constexpr int NS = PL::kStages, EW = PL::EW;
+__global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_constant__ GemmArgs a) {
+  constexpr int NS = kStages, EW = kEpiWarps;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + NS, *acc_full = empty + NS, *acc_empty = acc_full + 2;
@@ -278,6 +320,8 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
   if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // nothing above touched global memory
+  griddep_launch();
   GemmWalk walk(a, unit, units);
   GemmTile tl;
 
@@ -287,13 +331,13 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
     // lane that issued them all and looked them up spent 880 clocks a step on it, the MMAs take 512.
     uint32_t it = 0;
     bool ok = true;
-    const uint32_t tx = CG * (PL::kABytes + bl * kBK * 2);
+    const uint32_t tx = CG * (kABytes + bl * kBK * 2);
     while (ok && walk.next(a, tl)) {
       const GemmProb &p = a.p[tl.p];
-      const int per = tl.steps / p.segs, m0 = (tl.m0 * CG + rank) * 128, na = p.a_mn ? 2 : 1;
+      const int per = (p.k + kBK - 1) / kBK, m0 = (tl.m0 * CG + rank) * 128, na = p.a_mn ? 2 : 1;
       const bool is_a = lane < na, mine = lane < na + bl / 64, mn = is_a ? p.a_mn : p.b_mn;
       const int box = is_a ? lane : lane - na;
-      const uint32_t off = is_a ? box * 8192 : PL::kABytes + box * 8192;
+      const uint32_t off = is_a ? box * 8192 : kABytes + box * 8192;
       int row = is_a ? m0 + 64 * box : rank * bl + 64 * box, m_first = is_a ? p.a[0] : p.b[0], m_then = is_a ? p.a[1] : p.b[1];
       if (!is_a && EPI == kEpiSwiglu) {
         // the first half of the tile's B rows are Wg's, the second half the same rows of Wu
@@ -305,8 +349,9 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
       }
       const CUtensorMap *map = &a.map[m_first];
       const CUtensorMap *then = &a.map[m_then];
-      int k = 0;
-      for (int s = 0; s < tl.steps; ++s, ++it) {
+      if (tl.s0 > per) map = then;
+      int k = (tl.s0 > per ? tl.s0 - per : tl.s0) * kBK;
+      for (int s = tl.s0; s < tl.s0 + tl.steps; ++s, ++it) {
         const int st = it % NS;
         const bool got = it < NS || pf_wait(&empty[st], ((it / NS) - 1) & 1u, kSpin, abort_flag, err);
         if (!(ok = __all_sync(0xffffffffu, got))) break;
@@ -314,7 +359,7 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
         __syncwarp();
         if (s == per) map = then, k = 0;
         if (mine)
-          g_load<CG>(stages + st * PL::kStageBytes + off, map, mn ? row : k, mn ? k : row, &full[st],
+          g_load<CG>(stages + st * kStageBytes + off, map, mn ? row : k, mn ? k : row, &full[st],
                      CG == 2 ? leader_addr(&full[st]) : 0);
         k += kBK;
       }
@@ -340,14 +385,14 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
         const uint32_t idesc = (idesc_bf16(bn) & 0x00FFFFFFu) | (static_cast<uint32_t>(128 * CG >> 4) << 24) |
                                (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
         const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
-        const uint32_t sa = smem_u32(stages), sb = sa + PL::kABytes;
+        const uint32_t sa = smem_u32(stages), sb = sa + kABytes;
         const uint64_t ad0 = p.a_mn ? mn_desc(sa) : sw128_desc(sa), bd0 = p.b_mn ? mn_desc(sb) : sw128_desc(sb);
         const uint32_t acc = tmem + b * kMaxBN;
         for (int s = 0; s < tl.steps; ++s, ++it) {
           const int st = it % NS;
           if (!(ok = pf_wait(&full[st], (it / NS) & 1u, kSpin, abort_flag, err))) break;
           tc_fence_after();
-          const uint64_t ad = ad0 + (st * PL::kStageBytes >> 4), bd = bd0 + (st * PL::kStageBytes >> 4);
+          const uint64_t ad = ad0 + (st * kStageBytes >> 4), bd = bd0 + (st * kStageBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             g_mma<CG>(acc, ad + kk * a_step, bd + kk * b_step, idesc, s > 0 || kk > 0);
@@ -359,123 +404,147 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
     }
   } else {
     // ---------------- epilogue
-    float *scratch = reinterpret_cast<float *>(stages + NS * PL::kStageBytes + warp * 4096);
+    float *scratch = reinterpret_cast<float *>(stages + NS * kStageBytes + warp * 4096);
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     uint32_t n = 0;
     while (walk.next(a, tl)) {
       const int b = n & 1, rows = a.p[tl.p].m, cols = a.p[tl.p].n;
-      const int row0 = (tl.m0 * CG + rank) * 128 + 32 * (warp & 3);
+      const int row0 = (tl.m0 * CG + rank) * 128 + 32 * (warp & 3), first = 32 * (warp >> 2);
       const uint32_t acc = tmem + b * kMaxBN + quad;
-      // dswiglu: the first g and u are on their way while the accumulators are waited for
-      float4 gq[4], uq[4];
-      const int c = lane & 7;
-      auto fetch = [&](int h) {  // rows 16 (h % 2) .. of this warp's column chunk h / 2
-        const int col = tl.n0 * bn + 32 * (warp >> 2) + 8 * EW * (h >> 1) + 4 * c;
+      // dswiglu: a lane takes eight columns of a row of g, u and the results; the first g and u are on
+      // their way while the accumulators are waited for
+      float4 gq[2][2], uq[2][2];
+      const int c = lane & 3, r0 = lane >> 2;
+      auto fetch = [&](int c0, int h) {  // rows 16 h + 8 i + lane / 4 of the chunk at column c0
+        const int col = tl.n0 * bn + c0 + 8 * c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = row0 + 16 * (h & 1) + 4 * i + (lane >> 3);
+        for (int i = 0; i < 2; ++i) {
+          const int row = row0 + 16 * h + 8 * i + r0;
           if (row < rows && col < cols) {
-            gq[i] = *reinterpret_cast<const float4 *>(a.g + row * a.f_ld + col);
-            uq[i] = *reinterpret_cast<const float4 *>(a.u + row * a.f_ld + col);
+            const float4 *gp = reinterpret_cast<const float4 *>(a.g + row * a.f_ld + col);
+            const float4 *up = reinterpret_cast<const float4 *>(a.u + row * a.f_ld + col);
+            gq[i][0] = gp[0], gq[i][1] = gp[1], uq[i][0] = up[0], uq[i][1] = up[1];
           }
         }
       };
-      if (EPI == kEpiDswiglu) fetch(0);
+      if (EPI == kEpiDswiglu && first < bn) fetch(first, 0);
       if (!__all_sync(0xffffffffu, pf_wait(&acc_full[b], (n >> 1) & 1u, kSpin, abort_flag, err))) break;
       ++n;
       tc_fence_after();
-      if (EPI == kEpiSwiglu) {
-        const int half = bn / 2, cc = lane & 3;
-        float *gs = a.g, *us = a.u;
-        const int64_t ld = a.f_ld;
-        for (int c0 = 16 * (warp >> 2); c0 < half; c0 += 4 * EW) {
-          uint32_t v[32];
-          tmem_ld16_nowait(acc + c0, v);
-          tmem_ld16_nowait(acc + half + c0, v + 16);
-          tmem_wait_ld();
-          __syncwarp();
-          turn_in(scratch, v, lane);
-          __syncwarp();
-          const int col = tl.n0 * half + c0 + 4 * cc;
-          if (col < cols) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 8 * i + (lane >> 2), row = row0 + r;
-              const float4 gf = turn_out(scratch, r, cc), uf = turn_out(scratch, r, 4 + cc);
-              if (row >= rows) continue;
-              const int64_t at = row * ld + col;
-              const float gv[4] = {gf.x, gf.y, gf.z, gf.w}, uv[4] = {uf.x, uf.y, uf.z, uf.w};
-              float hv[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) hv[k] = gv[k] * sigmoid_f(gv[k]) * uv[k];
-              put4(a.h + at, hv);
-              if (gs) {
-                put4(gs + at, gv);
-                put4(us + at, uv);
-              }
-            }
-          }
+      // the accumulators are handed back as soon as this warp's last chunk is in registers, before its
+      // stores: a release at cluster scope after them would wait for all of them (2,000 clocks)
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(&acc_empty[b])) : "memory");
+          else
+            mbar_arrive(&acc_empty[b]);
         }
-      } else {
+      };
+      if (EPI == kEpiSwiglu) {
+        const int half = bn / 2, col = tl.n0 * half + first;  // at most one chunk of g and u a warp
+        if (first < half) {
+          uint32_t v[32], w[32];
+          tmem_ld32_nowait(acc + first, v);
+          tmem_ld32_nowait(acc + half + first, w);
+          tmem_wait_ld();
+          release();
+          if (a.g) {
+            store_f32(scratch, v, lane, a.g, a.f_ld, row0, rows, col, cols);
+            store_f32(scratch, w, lane, a.u, a.f_ld, row0, rows, col, cols);
+          }
+          uint32_t h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
+            h[i] = pack2(g0 * sigmoid_f(g0) * __uint_as_float(w[2 * i]), g1 * sigmoid_f(g1) * __uint_as_float(w[2 * i + 1]));
+          }
+          store_bf16(scratch, h, lane, a.h, a.f_ld, row0, rows, col, cols);
+        } else {
+          release();
+        }
+      } else if (EPI == kEpiPlain) {
         const void *add = a.p[tl.p].add;
         void *out = a.p[tl.p].out;
         const int64_t ld = a.p[tl.p].ld, add_ld = a.p[tl.p].add_ld;
         const int out_bf16 = a.p[tl.p].out_bf16, add_bf16 = a.p[tl.p].add_bf16;
-        auto half = [&](int h) {
-          const int col = tl.n0 * bn + 32 * (warp >> 2) + 8 * EW * (h >> 1) + 4 * c;
-          if (col >= cols) return;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 16 * (h & 1) + 4 * i + (lane >> 3), row = row0 + r;
-            const float4 q = turn_out(scratch, r, c);
-            if (row >= rows) continue;
-            float d[4] = {q.x, q.y, q.z, q.w};
-            if (EPI == kEpiDswiglu) {
-              const int64_t at = row * a.f_ld + col;
-              const float gv[4] = {gq[i].x, gq[i].y, gq[i].z, gq[i].w}, uv[4] = {uq[i].x, uq[i].y, uq[i].z, uq[i].w};
-              float hv[4], dg[4], du[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float sg = sigmoid_f(gv[k]), sl = gv[k] * sg;
-                hv[k] = sl * uv[k];
-                du[k] = d[k] * sl;
-                dg[k] = d[k] * uv[k] * fmaf(sl, 1.f - sg, sg);
-              }
-              put4(a.h + at, hv);
-              put4(a.dg + at, dg);
-              put4(a.du + at, du);
-            } else {
-              if (add) {
-                const float4 e = get4(add, row * add_ld + col, add_bf16);
-                d[0] += e.x; d[1] += e.y; d[2] += e.z; d[3] += e.w;
-              }
-              if (out_bf16)
-                put4(static_cast<__nv_bfloat16 *>(out) + row * ld + col, d);
-              else
-                put4(static_cast<float *>(out) + row * ld + col, d);
-            }
-          }
-        };
-        for (int c0 = 32 * (warp >> 2), h = 0; c0 < bn; c0 += 8 * EW, h += 2) {
-          if (EPI == kEpiDswiglu && h) fetch(h);
+        float *fout = static_cast<float *>(out) + tl.split * a.p[tl.p].split_ld;
+        if (first >= bn) release();
+        for (int c0 = first; c0 < bn; c0 += 8 * EW) {
           uint32_t v[32];
           tmem_ld32_nowait(acc + c0, v);
           tmem_wait_ld();
+          if (c0 + 8 * EW >= bn) release();
+          const int col = tl.n0 * bn + c0;
+          if (add) {
+            // added a row a lane: whole sectors of that row
+            const int row = row0 + lane;
+            if (row < rows) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                if (col + i < cols) {
+                  const float4 e = get4(add, row * add_ld + col + i, add_bf16);
+                  const float f[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) v[i + k] = __float_as_uint(__uint_as_float(v[i + k]) + f[k]);
+                }
+            }
+            __syncwarp();
+          }
+          if (out_bf16) {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            store_bf16(scratch, h, lane, static_cast<__nv_bfloat16 *>(out), ld, row0, rows, col, cols);
+          } else {
+            store_f32(scratch, v, lane, fout, ld, row0, rows, col, cols);
+          }
+        }
+      } else {
+        if (first >= bn) release();
+        for (int c0 = first; c0 < bn; c0 += 8 * EW) {
+          if (c0 != first) fetch(c0, 0);
+          uint32_t v[32];
+          tmem_ld32_nowait(acc + c0, v);
+          tmem_wait_ld();
+          if (c0 + 8 * EW >= bn) release();
           __syncwarp();
           turn_in(scratch, v, lane);
           __syncwarp();
-          half(h);
-          if (EPI == kEpiDswiglu) fetch(h + 1);
-          half(h + 1);
+          const int col = tl.n0 * bn + c0 + 8 * c;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h) fetch(c0, 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 16 * h + 8 * i + r0, row = row0 + r;
+              const float4 d0 = turn_out(scratch, r, 2 * c), d1 = turn_out(scratch, r, 2 * c + 1);
+              if (row >= rows || col >= cols) continue;
+              const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+              const float gv[8] = {gq[i][0].x, gq[i][0].y, gq[i][0].z, gq[i][0].w, gq[i][1].x, gq[i][1].y, gq[i][1].z, gq[i][1].w};
+              const float uv[8] = {uq[i][0].x, uq[i][0].y, uq[i][0].z, uq[i][0].w, uq[i][1].x, uq[i][1].y, uq[i][1].z, uq[i][1].w};
+              uint32_t hv[4], dg[4], du[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float x[2][3];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float g = gv[2 * k + e], sg = sigmoid_f(g), sl = g * sg;
+                  x[e][0] = sl * uv[2 * k + e];
+                  x[e][1] = d[2 * k + e] * uv[2 * k + e] * fmaf(sl, 1.f - sg, sg);
+                  x[e][2] = d[2 * k + e] * sl;
+                }
+                hv[k] = pack2(x[0][0], x[1][0]), dg[k] = pack2(x[0][1], x[1][1]), du[k] = pack2(x[0][2], x[1][2]);
+              }
+              const int64_t at = row * a.f_ld + col;
+              *reinterpret_cast<uint4 *>(a.h + at) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              *reinterpret_cast<uint4 *>(a.dg + at) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+              *reinterpret_cast<uint4 *>(a.du + at) = make_uint4(du[0], du[1], du[2], du[3]);
+            }
+          }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(&acc_empty[b])) : "memory");
-        else
-          mbar_arrive(&acc_empty[b]);
       }
     }
   }
@@ -485,6 +554,36 @@ __global__ void __launch_bounds__(GemmPlan<EPI, CG>::kThreads, 1) k_ffn_gemm(con
   // a CTA's shared memory is read by the pair's MMAs and its barriers are arrived on by the other CTA
   if (CG == 2) cluster_sync();
   if (warp == 0) g_tmem_dealloc<CG>(tmem);
+}
+
+// out = sum of the pieces of a split product, in order, (+ add)
+struct SumArgs {
+  const float *part;
+  const void *add;
+  void *out;
+  int64_t ld, add_ld, split_ld;
+  int m, n, splits, out_bf16, add_bf16;
+};
+__global__ void __launch_bounds__(256) k_ffn_sum(SumArgs a) {
+  griddep_wait();
+  griddep_launch();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= static_cast<int64_t>(a.m) * a.n) return;
+  const int64_t row = i / a.n, col = i - row * a.n;
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 q = *reinterpret_cast<const float4 *>(a.part + s * a.split_ld + i);
+    d[0] += q.x; d[1] += q.y; d[2] += q.z; d[3] += q.w;
+  }
+  if (a.add) {
+    const float4 e = get4(a.add, row * a.add_ld + col, a.add_bf16);
+    d[0] += e.x; d[1] += e.y; d[2] += e.z; d[3] += e.w;
+  }
+  if (a.out_bf16)
+    put4(static_cast<__nv_bfloat16 *>(a.out) + row * a.ld + col, d);
+  else
+    put4(static_cast<float *>(a.out) + row * a.ld + col, d);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -550,6 +649,8 @@ template <int NT>
 __global__ void __launch_bounds__(kSmThreads) k_ffn_up(SmallArgs a) {
   __shared__ float red[(kSmWarps - 1) * NT * 4 * 32];
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, row = blockIdx.x * 8 + g;
+  griddep_wait();
+  griddep_launch();
   float acc[NT][4] = {};
   const bool ok = row < a.f;
   small_mma<NT>(a.wg + static_cast<int64_t>(row) * a.d, a.wu + static_cast<int64_t>(row) * a.d, ok, ok, a.x, a.x_ld, a.n,
@@ -576,6 +677,8 @@ template <int NT>
 __global__ void __launch_bounds__(kSmThreads) k_ffn_down(SmallArgs a) {
   __shared__ float red[(kSmWarps - 1) * NT * 4 * 32];
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, r0 = blockIdx.x * 16 + g, r1 = r0 + 8;
+  griddep_wait();
+  griddep_launch();
   float acc[NT][4] = {};
   small_mma<NT>(a.wd + static_cast<int64_t>(r0) * a.f, a.wd + static_cast<int64_t>(r1) * a.f, r0 < a.d, r1 < a.d, a.h,
                 a.f, a.n, a.f, acc);
@@ -608,25 +711,32 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
 
 template <int EPI>
 cudaError_t configure_gemm() {
-  cudaError_t e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmPlan<EPI, 1>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmPlan<EPI, 2>::kSmem);
+    e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   return e;
 }
 
-template <int EPI>
-void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int grid, cudaStream_t st) {
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(GemmPlan<EPI, 2>::kThreads);
-  cfg.dynamicSmemBytes = GemmPlan<EPI, 2>::kSmem;
-  cfg.stream = st;
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-}
+// Launch configuration: clusters of cg CTAs, programmatic stream serialization (the kernel may begin
+// while the one before it ends; it waits for that one's results itself).
+struct Config {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2];
+  Config(int grid, int threads, int smem, int cg, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cg;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cg > 1 ? 2 : 1;
+  }
+};
 
 struct FfnDevice {
   EncodeFn encode;
@@ -655,10 +765,8 @@ cudaError_t ffn_setup(FfnDevice *out) {
     if (e == cudaSuccess) e = configure_gemm<kEpiSwiglu>();
     if (e == cudaSuccess) e = configure_gemm<kEpiDswiglu>();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    pair_config<kEpiPlain>(cfg, at, 2, nullptr);
-    e = cudaOccupancyMaxActiveClusters(&k.pairs, k_ffn_gemm<kEpiPlain, 2>, &cfg);
+    const Config two(2, kGemmThreads, kGemmSmem, 2, nullptr);
+    e = cudaOccupancyMaxActiveClusters(&k.pairs, k_ffn_gemm<kEpiPlain, 2>, &two.cfg);
     if (e != cudaSuccess) return e;
     if (k.pairs > k.nsm / 2) k.pairs = k.nsm / 2;
     k.encode = reinterpret_cast<EncodeFn>(fn);
@@ -689,7 +797,7 @@ struct Maps {
 
 GemmProb &add_prob(GemmArgs &a, int m, int n, int k) {
   GemmProb &p = a.p[a.n_prob++];
-  p.m = m, p.n = n, p.k = k, p.segs = 1;
+  p.m = m, p.n = n, p.k = k, p.segs = p.splits = 1;
   return p;
 }
 
@@ -701,18 +809,19 @@ cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
   struct Form {
     int cg, bn, step;
   };
-  constexpr Form forms[] = {{2, 256, 520}, {1, 256, 640}, {1, 128, 400}, {1, 64, 320}};
+  constexpr Form forms[] = {{2, 256, 800}, {2, 128, 560}, {1, 128, 560}, {1, 64, 420}};
   double best = 0;
   Form f{};
   for (const Form &c : forms) {
+    if (a.p[0].splits > 1 && (c.cg != 1 || c.bn != 128)) continue;
     if (EPI == kEpiSwiglu && c.bn == 64) continue;  // 64 rows each of two matrices at least
     const int cols = EPI == kEpiSwiglu ? c.bn / 2 : c.bn, units = c.cg == 2 ? dev.pairs : dev.nsm;
     if (units < 1) continue;
     double steps = 0, longest = 0;  // of all tiles and of the longest
     for (int i = 0; i < a.n_prob; ++i) {
       const GemmProb &p = a.p[i];
-      const double len = p.segs * ((p.k + kBK - 1) / kBK) + 4;  // 4: filling and draining
-      const double tiles = static_cast<double>((p.m + 128 * c.cg - 1) / (128 * c.cg)) * ((p.n + cols - 1) / cols);
+      const double len = p.segs * ((p.k + kBK - 1) / kBK) / p.splits + 4;  // 4: filling and draining
+      const double tiles = static_cast<double>((p.m + 128 * c.cg - 1) / (128 * c.cg)) * ((p.n + cols - 1) / cols) * p.splits;
       // alone, whole rounds of tiles; among others, what is left over is filled up
       steps += a.n_prob == 1 ? len * units * static_cast<int>((tiles + units - 1) / units) : len * tiles;
       longest = longest > len ? longest : len;
@@ -727,17 +836,18 @@ cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
     GemmProb &p = a.p[i];
     p.tiles_m = (p.m + 128 * f.cg - 1) / (128 * f.cg);
     p.tiles_n = (p.n + cols - 1) / cols;
-    tiles += p.tiles_m * p.tiles_n;
+    tiles += p.tiles_m * p.tiles_n * p.splits;
   }
   const int units = f.cg == 2 ? dev.pairs : dev.nsm, grid = (tiles < units ? tiles : units) * f.cg;
-  if (f.cg == 1) {
-    k_ffn_gemm<EPI, 1><<<grid, GemmPlan<EPI, 1>::kThreads, GemmPlan<EPI, 1>::kSmem, st>>>(a);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  pair_config<EPI>(cfg, at, grid, st);
-  return cudaLaunchKernelEx(&cfg, k_ffn_gemm<EPI, 2>, a);
+  const Config c(grid, kGemmThreads, kGemmSmem, f.cg, st);
+  return f.cg == 1 ? cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 1>, a) : cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 2>, a);
+}
+
+template <int NT>
+cudaError_t launch_small(const SmallArgs &s, int up, int down, cudaStream_t st) {
+  const Config cu(up, kSmThreads, 0, 1, st), cd(down, kSmThreads, 0, 1, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cu.cfg, k_ffn_up<NT>, s);
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cd.cfg, k_ffn_down<NT>, s) : e;
 }
 
 constexpr int kMaxDim = 65536;
@@ -750,12 +860,44 @@ bool bad_shape(int n, int d, int f) {
 }
 uint64_t align_ws(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
+// Pieces of the k range (k values) of a product with n x d results: where these make fewer tiles of
+// 128 x 128 than a B200 has SMs, as many pieces as fill it, each of eight steps at least.  300 tokens,
+// d 2,048, f 8,192: the down product takes 49 us in one piece, its weights' bytes 5.
+int product_splits(int n, int d, int64_t k) {
+  const int64_t tiles = static_cast<int64_t>((n + 127) / 128) * ((d + 127) / 128), steps = (k + kBK - 1) / kBK;
+  int64_t s = tiles ? 148 / tiles : 1;
+  if (s > steps / 8) s = steps / 8;
+  return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
+}
+uint64_t split_bytes(int n, int d, int64_t k) {
+  const int s = product_splits(n, d, k);
+  return s > 1 ? align_ws(static_cast<uint64_t>(s) * n * d * 4) : 0;
+}
+
+// Sends a product's result through the pieces at `part` where it is split, and adds them up after the
+// launch.
+struct Split {
+  SumArgs sum{};
+  void set(GemmProb &q, float *part, int splits) {
+    q.splits = splits;
+    if (splits < 2) return;
+    sum = SumArgs{part, q.add, q.out, q.ld, q.add_ld, static_cast<int64_t>(q.m) * q.n, q.m, q.n, splits, q.out_bf16, q.add_bf16};
+    q.out = part, q.ld = q.n, q.out_bf16 = 0, q.add = nullptr, q.split_ld = sum.split_ld;
+  }
+  cudaError_t run(cudaStream_t st) const {
+    if (sum.splits < 2) return cudaSuccess;
+    const Config c(static_cast<int>((sum.split_ld / 4 + 255) / 256), 256, 0, 1, st);
+    return cudaLaunchKernelEx(&c.cfg, k_ffn_sum, sum);
+  }
+};
+
 }  // namespace
 
 extern "C" uint64_t moe_ffn_workspace(int32_t n_tokens, int32_t d_model, int32_t d_ff, int32_t backward) {
   if (bad_shape(n_tokens, d_model, d_ff)) return 0;
   const uint64_t nf = align_ws(static_cast<uint64_t>(n_tokens) * d_ff * 2);
-  return backward ? 3 * nf : nf;
+  if (backward) return 3 * nf + split_bytes(n_tokens, d_model, 2 * static_cast<int64_t>(d_ff));
+  return nf + (n_tokens > kSmallMax ? split_bytes(n_tokens, d_model, d_ff) : 0);
 }
 
 extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
@@ -782,13 +924,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     s.h = h, s.g = static_cast<float *>(p->save_gate), s.u = static_cast<float *>(p->save_up);
     s.n = n, s.d = d, s.f = f;
     const int gu = (f + 7) / 8, gd = (d + 15) / 16;
-    if (n <= 8)
-      k_ffn_up<1><<<gu, kSmThreads, 0, st>>>(s), k_ffn_down<1><<<gd, kSmThreads, 0, st>>>(s);
-    else if (n <= 16)
-      k_ffn_up<2><<<gu, kSmThreads, 0, st>>>(s), k_ffn_down<2><<<gd, kSmThreads, 0, st>>>(s);
-    else
-      k_ffn_up<4><<<gu, kSmThreads, 0, st>>>(s), k_ffn_down<4><<<gd, kSmThreads, 0, st>>>(s);
-    e = cudaGetLastError();
+    e = n <= 8 ? launch_small<1>(s, gu, gd, st) : n <= 16 ? launch_small<2>(s, gu, gd, st) : launch_small<4>(s, gu, gd, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   FfnDevice dev{};
@@ -809,6 +945,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
   }
   if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
   GemmArgs b{};
+  Split split;
   {
     Maps m{dev.encode, b};
     GemmProb &q = add_prob(b, n, d, f);
@@ -816,9 +953,11 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     q.b[0] = m.add(p->w_down, d, f, f, 64);
     q.out = p->y, q.ld = p->y_stride, q.out_bf16 = p->y_dtype == MOE_BF16;
     q.add = p->add, q.add_ld = p->add_stride, q.add_bf16 = p->add_dtype == MOE_BF16;
+    split.set(q, reinterpret_cast<float *>(h + align_ws(static_cast<uint64_t>(n) * f * 2) / 2), product_splits(n, d, f));
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
   e = launch_gemm<kEpiPlain>(b, dev, st);
+  if (e == cudaSuccess) e = split.run(st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -855,12 +994,22 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
   // everything else in one launch: dx (its tiles run over both matrices), then the weights' gradients
   GemmArgs a{};
   Maps m{dev.encode, a};
+  Split split;
   if (p->dx) {
     GemmProb &q = add_prob(a, n, d, f);
     q.segs = 2;
     q.a[0] = m.add(dg, n, f, f, 128), q.a[1] = m.add(du, n, f, f, 128);
     q.b[0] = m.add(p->w_gate, f, d, d, kBK), q.b[1] = m.add(p->w_up, f, d, d, kBK), q.b_mn = 1;
     q.out = p->dx, q.ld = p->dx_stride, q.out_bf16 = 1;
+    split.set(q, reinterpret_cast<float *>(du + nf), product_splits(n, d, 2 * static_cast<int64_t>(f)));
+    // split, few tokens: the weights' gradients have other shapes of tiles, a launch of their own
+    if (q.splits > 1) {
+      if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
+      e = launch_gemm<kEpiPlain>(a, dev, st);
+      if (e == cudaSuccess) e = split.run(st);
+      if (e != cudaSuccess) return MOE_ERR_CUDA;
+      a.n_prob = m.n = 0;
+    }
   }
   if (p->dw_gate) {
     const int mx = m.add(p->x, n, d, p->x_stride, kBK);
@@ -877,8 +1026,8 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     q.out = p->dw_down, q.ld = f, q.out_bf16 = 1;
   }
   if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-  e = launch_gemm<kEpiPlain>(a, dev, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (a.n_prob && (e = launch_gemm<kEpiPlain>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 extern "C" moe_status moe_ffn_check(void) {
