@@ -120,7 +120,7 @@ EXPORTED = [
     "moe_norm_in", "moe_norm_out", "moe_norm_workspace", "moe_norm_in_backward", "moe_norm_out_backward",
     "moe_adapters_create", "moe_adapters_load", "moe_adapters_apply", "moe_adapters_check", "moe_adapters_destroy",
     "moe_adapters_last_error", "moe_adapters_device_bytes",
-    "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_check",
+    "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward", "moe_block_check",
     "moe_blocks_workspace", "moe_forward_blocks",
 ]
 
@@ -175,13 +175,13 @@ def lib() -> C.CDLL:
         L.moe_adapters_device_bytes.restype = U64
         L.moe_ffn_workspace.argtypes = [I, I, I, I]
         L.moe_ffn_workspace.restype = U64
-        L.moe_ffn_check.argtypes = []
+        L.moe_block_check.argtypes = []
         L.moe_blocks_workspace.argtypes = [P, P, I, I]
         L.moe_blocks_workspace.restype = U64
         L.moe_forward_blocks.argtypes = [P, I, I, P, P, P, I, P, P, U64, P, C.POINTER(moe_route_out)]
         for name in ("moe_norm_in", "moe_norm_out", "moe_norm_in_backward", "moe_norm_out_backward",
                      "moe_adapters_create", "moe_adapters_load", "moe_adapters_apply", "moe_adapters_check",
-                     "moe_adapters_destroy", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_check",
+                     "moe_adapters_destroy", "moe_ffn_forward", "moe_ffn_backward", "moe_block_check",
                      "moe_forward_blocks"):
             getattr(L, name).restype = I
         for name in ("moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack", "moe_check",
@@ -380,7 +380,7 @@ class MoE:
 
 # The block operators' wrappers (block.py) need torch, which this module only imports when it is used.
 _BLOCK = ("norm_in", "norm_out", "norm_in_backward", "norm_out_backward", "Adapters", "ffn_forward", "ffn_backward",
-          "ffn_check", "Block")
+          "block_check", "Block")
 
 
 def __getattr__(name):

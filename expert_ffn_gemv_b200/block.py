@@ -196,9 +196,9 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, need_dx=True, need_dw=Tr
     return _ext.ffn_backward(dy, x, w_gate, w_up, w_down, g, u, need_dx, need_dw)
 
 
-def ffn_check() -> int:
-    """Waits for the current device; MOE_ERR_TIMEOUT if a wait of the dense block's kernels ran out."""
-    return _lib.moe_ffn_check()
+def block_check() -> int:
+    """Waits for the current device; MOE_ERR_TIMEOUT if a wait of the norms' or the dense block's kernels ran out."""
+    return _lib.moe_block_check()
 
 
 # -------------------------------------------------------------------------------------- one block

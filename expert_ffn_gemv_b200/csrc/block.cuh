@@ -11,6 +11,9 @@ namespace moe {
 // Whether the handle adapts d -> d on this device and takes n tokens a call (adapters.cu).
 bool adapters_match(const moe_adapters *h, int d, int device, int n);
 
+// Reads and clears the norms' error word on the current device (norms.cu).
+cudaError_t take_norm_error(uint32_t *err);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SMs of the current device (asked once per device).

@@ -26,7 +26,7 @@ constexpr int kMaxBN = 256;
 constexpr uint64_t kSpin = 2000000000ull;  // about a second
 constexpr int kMaxProb = 4, kMaxMaps = 9;
 
-// Set by a kernel whose bounded wait ran out; moe_ffn_check reads and clears it.
+// Set by a kernel whose bounded wait ran out; moe_block_check reads and clears it.
 __device__ uint32_t g_ffn_err;
 
 enum { kEpiPlain = 0, kEpiSwiglu = 1, kEpiDswiglu = 2 };
@@ -1030,17 +1030,17 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
   return MOE_OK;
 }
 
-extern "C" moe_status moe_ffn_check(void) {
-  uint32_t v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_ffn_err, sizeof v) != cudaSuccess) {
+extern "C" moe_status moe_block_check(void) {
+  uint32_t v = 0, w = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_ffn_err, sizeof v);
+  if (e == cudaSuccess) e = take_norm_error(&w);
+  if (e == cudaSuccess && v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_ffn_err, &zero, sizeof zero);
+  }
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  if (!v) return MOE_OK;
-  v = 0;
-  if (cudaMemcpyToSymbol(g_ffn_err, &v, sizeof v) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  return MOE_ERR_TIMEOUT;
+  return v || w ? MOE_ERR_TIMEOUT : MOE_OK;
 }

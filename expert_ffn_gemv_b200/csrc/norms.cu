@@ -15,37 +15,52 @@
 // the same call gives the same bits.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "block.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kNormMaxD = 8192;      // V * NCH * threads
-constexpr int kNormMaxThreads = 256;
+constexpr int kNormMaxD = 8192;  // V * NCH * threads
 
+// V consecutive values (V = 1, 2, 4 or 8: the widest that width, pointers and strides allow)
 template <int V>
 __device__ __forceinline__ void load_v(const void *p, int64_t i, int bf16, float (&v)[V]) {
   if (bf16) {
     const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p) + i;
-    if constexpr (V == 8) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(b);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (V == 1) {
+      v[0] = __bfloat162float(*b);
+    } else {
+      uint32_t w[V / 2];
+      if constexpr (V == 8) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(b);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+      } else if constexpr (V == 4) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(b);
+        w[0] = q.x, w[1] = q.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(b);
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < V / 2; ++k) {
         v[2 * k] = __uint_as_float(w[k] << 16);
         v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
       }
-    } else {
-      v[0] = __bfloat162float(*b);
     }
   } else {
     const float *f = static_cast<const float *>(p) + i;
-    if constexpr (V == 8) {
-      const float4 a = *reinterpret_cast<const float4 *>(f), c = *reinterpret_cast<const float4 *>(f + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
-    } else {
+    if constexpr (V == 1) {
       v[0] = *f;
+    } else if constexpr (V == 2) {
+      const float2 a = *reinterpret_cast<const float2 *>(f);
+      v[0] = a.x, v[1] = a.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(f + k);
+        v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+      }
     }
   }
 }
@@ -55,56 +70,118 @@ template <int V>
 __device__ __forceinline__ void store_v(void *p, int64_t i, int bf16, float (&v)[V]) {
   if (bf16) {
     __nv_bfloat16 *b = static_cast<__nv_bfloat16 *>(p) + i;
-    if constexpr (V == 8) {
-      __nv_bfloat162 h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-        const float2 f = __bfloat1622float2(h[k]);
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
-      }
-      *reinterpret_cast<uint4 *>(b) = *reinterpret_cast<const uint4 *>(h);
-    } else {
+    if constexpr (V == 1) {
       const __nv_bfloat16 h = __float2bfloat16_rn(v[0]);
       *b = h;
       v[0] = __bfloat162float(h);
+    } else {
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t *>(&h);
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+      if constexpr (V == 8)
+        *reinterpret_cast<uint4 *>(b) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(b) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t *>(b) = w[0];
     }
   } else {
     float *f = static_cast<float *>(p) + i;
-    if constexpr (V == 8) {
-      *reinterpret_cast<float4 *>(f) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(f + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
+    if constexpr (V == 1) {
       *f = v[0];
+    } else if constexpr (V == 2) {
+      *reinterpret_cast<float2 *>(f) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) *reinterpret_cast<float4 *>(f + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
     }
   }
 }
 
-// Sums of NV values over the block, in every thread; `red` holds 8 warps x NV and is used in turn
-// with a second buffer (`red` flips), so one barrier a call is enough.
+// A thread's values of a row: columns (256 c + thread) V .. + V - 1, c < NCH, below d.  (A block of
+// fewer threads holds its row in c = 0.)  One branch on the type for all of a row's loads.
+constexpr int kNormMaxThreads = 256;
+template <int V, int NCH>
+__device__ __forceinline__ void load_row(const void *p, int64_t first, int bf16, int d, float (&v)[NCH][V]) {
+  const int i0 = threadIdx.x * V;
+  if (bf16) {
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p) + first + i0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (i0 + c * kNormMaxThreads * V < d) load_v<V>(q, c * kNormMaxThreads * V, 1, v[c]);
+  } else {
+    const float *q = static_cast<const float *>(p) + first + i0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (i0 + c * kNormMaxThreads * V < d) load_v<V>(q, c * kNormMaxThreads * V, 0, v[c]);
+  }
+}
+template <int V, int NCH>
+__device__ __forceinline__ void store_row(void *p, int64_t first, int bf16, int d, float (&v)[NCH][V]) {
+  const int i0 = threadIdx.x * V;
+  if (bf16) {
+    __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(p) + first + i0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (i0 + c * kNormMaxThreads * V < d) store_v<V>(q, c * kNormMaxThreads * V, 1, v[c]);
+  } else {
+    float *q = static_cast<float *>(p) + first + i0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      if (i0 + c * kNormMaxThreads * V < d) store_v<V>(q, c * kNormMaxThreads * V, 0, v[c]);
+  }
+}
+// f(value index in the thread) for all of them
+#define MOE_EACH(c, k)             \
+  _Pragma("unroll") for (int c = 0; c < NCH; ++c) _Pragma("unroll") for (int k = 0; k < V; ++k)
+
+template <int V, int NCH>
+__device__ __forceinline__ void fill(float (&v)[NCH][V], float x) {
+  MOE_EACH(c, k) v[c][k] = x;
+}
+
+// Sums of NV values over `threads` threads of the block, in every one of them: shuffles, then the warps'
+// sums in order.  red: [NV][8], zeros where there is no warp (clear_sums); calls take turns with two of
+// them, so one barrier a call is enough.
 template <int NV>
-__device__ __forceinline__ void block_sum(float (&v)[NV], float *red) {
+__device__ __forceinline__ void block_sum(float (&v)[NV], float *red, int threads) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
-  if (warps == 1) return;
+    for (int k = 0; k < NV; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (threads == 32) return;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < NV; ++k) red[warp * NV + k] = v[k];
-  __syncthreads();
+    for (int k = 0; k < NV; ++k) red[8 * k + (threadIdx.x >> 5)] = v[k];
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    float s = red[k];
-    for (int w = 1; w < warps; ++w) s += red[w * NV + k];
-    v[k] = s;
+    const float4 p = *reinterpret_cast<const float4 *>(red + 8 * k), q = *reinterpret_cast<const float4 *>(red + 8 * k + 4);
+    v[k] = ((((((p.x + p.y) + p.z) + p.w) + q.x) + q.y) + q.z) + q.w;
   }
+}
+// Before the first sum; the caller's next barrier over the block comes after it.
+template <int N>
+__device__ __forceinline__ void clear_sums(float (&red)[N]) {
+  for (int i = threadIdx.x; i < N; i += 32)
+    if (threadIdx.x < 32) red[i] = 0.f;
+  __syncthreads();
 }
 
 __device__ __forceinline__ float gate_value(float g, int act) {
-  return act == MOE_GATE_SIGMOID ? 1.0f / (1.0f + __expf(-g)) : g;
+  if (act != MOE_GATE_SIGMOID) return g;
+  float r;  // approximate reciprocal (1 ulp; of infinity: 0): an IEEE division takes ten instructions
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+  return r;
+}
+template <int V, int NCH>
+__device__ __forceinline__ void gate_values(float (&g)[NCH][V], int act) {
+  if (act == MOE_GATE_SIGMOID) MOE_EACH(c, k) g[c][k] = gate_value(g[c][k], MOE_GATE_SIGMOID);
 }
 
 struct NormFwd {
@@ -113,86 +190,84 @@ struct NormFwd {
   int64_t o_ld, res_ld, gate_ld, out_ld, h_ld;
   int o_bf16, res_bf16, out_bf16, w_bf16, gate_bf16, h_bf16;
   int gate_kind, gate_act, d;
-  float eps, next_eps, scale, w_off;
+  float eps, next_eps, scale, w_off, inv_d;
 };
 
-// One block per token; thread t holds columns (c blockDim + t) V .. + V - 1, c < NCH.
+// A row's gate is per value (of its own, or one per column).
+__device__ __forceinline__ bool gate_by_value(int kind) { return kind == MOE_GATE_CHANNEL || kind == MOE_GATE_FULL; }
+
+// weight + unit offset; zeros past d
 template <int V, int NCH>
-__global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd(const __grid_constant__ NormFwd a) {
-  __shared__ float red[16];
-  const int64_t t = blockIdx.x;
-  const int d = a.d;
-  float r[NCH][V];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i = (c * blockDim.x + threadIdx.x) * V;
-    if (i < d)
-      load_v<V>(a.res, t * a.res_ld + i, a.res_bf16, r[c]);
-    else
-#pragma unroll
-      for (int k = 0; k < V; ++k) r[c][k] = 0.f;
+__device__ __forceinline__ void load_weight(const void *p, int bf16, int d, float off, float (&w)[NCH][V]) {
+  load_row<V, NCH>(p, 0, bf16, d, w);
+  if (off != 0.f) {
+    const int i0 = threadIdx.x * V;
+    MOE_EACH(c, k) if (i0 + c * kNormMaxThreads * V < d) w[c][k] += off;
   }
+}
+
+// What follows a row's loads.  Values past d are zeros everywhere.  The weights come in registers (KEEP,
+// with the offset added) or are loaded where they are used; `active`: g holds a(g) already.
+template <int V, int NCH, bool KEEP>
+__device__ __forceinline__ void fwd_row(const NormFwd &a, int64_t t, float (&r)[NCH][V], float (&o)[NCH][V], float (&g)[NCH][V],
+                                        float (&w)[NCH][V], float (&wn)[NCH][V], float gt, float *red, int threads,
+                                        bool active) {
+  const int d = a.d;
   if (a.o) {
-    float o[NCH][V];
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int i = (c * blockDim.x + threadIdx.x) * V;
-      if (i < d) load_v<V>(a.o, t * a.o_ld + i, a.o_bf16, o[c]);
-    }
-    float q = 1.f;
+    const bool by_value = gate_by_value(a.gate_kind);
+    const float f = a.scale * gt;
     if (a.w) {
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int i = (c * blockDim.x + threadIdx.x) * V;
-        if (i < d)
-#pragma unroll
-          for (int k = 0; k < V; ++k) ss[0] = fmaf(o[c][k], o[c][k], ss[0]);
-      }
-      block_sum<1>(ss, red);
-      q = rsqrtf(ss[0] / d + a.eps);
+      float ss[1] = {0.f};
+      MOE_EACH(c, k) ss[0] = fmaf(o[c][k], o[c][k], ss[0]);
+      if (!KEEP) load_weight<V, NCH>(a.w, a.w_bf16, d, a.w_off, w);
+      block_sum<1>(ss, red, threads);
+      const float q = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+      MOE_EACH(c, k) o[c][k] *= q * w[c][k];
     }
-    float gt = 1.f;
-    if (a.gate_kind == MOE_GATE_TOKEN) {
-      float g1[1];
-      load_v<1>(a.gate, t * a.gate_ld, a.gate_bf16, g1);
-      gt = gate_value(g1[0], a.gate_act);
+    if (by_value) {
+      if (!active) gate_values<V, NCH>(g, a.gate_act);
+      MOE_EACH(c, k) r[c][k] = fmaf(f * g[c][k], o[c][k], r[c][k]);
+    } else {
+      MOE_EACH(c, k) r[c][k] = fmaf(f, o[c][k], r[c][k]);
     }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int i = (c * blockDim.x + threadIdx.x) * V;
-      if (i >= d) continue;
-      float w[V], g[V];
-      if (a.w) load_v<V>(a.w, i, a.w_bf16, w);
-      if (a.gate_kind >= MOE_GATE_CHANNEL && a.gate_kind != MOE_GATE_TOKEN)
-        load_v<V>(a.gate, (a.gate_kind == MOE_GATE_FULL ? t * a.gate_ld : 0) + i, a.gate_bf16, g);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float u = a.w ? o[c][k] * q * (w[k] + a.w_off) : o[c][k];
-        const float av = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL ? gate_value(g[k], a.gate_act) : gt;
-        r[c][k] = fmaf(a.scale * av, u, r[c][k]);
-      }
-      store_v<V>(a.res_out, t * a.out_ld + i, a.out_bf16, r[c]);
-    }
+    store_row<V, NCH>(a.res_out, t * a.out_ld, a.out_bf16, d, r);
   }
   if (!a.h) return;
   float ss[1] = {0.f};
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
-    for (int k = 0; k < V; ++k) ss[0] = fmaf(r[c][k], r[c][k], ss[0]);
-  block_sum<1>(ss, red + 8);
-  const float p = rsqrtf(ss[0] / d + a.next_eps);
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i = (c * blockDim.x + threadIdx.x) * V;
-    if (i >= d) continue;
-    float w[V];
-    load_v<V>(a.next_w, i, a.w_bf16, w);
-#pragma unroll
-    for (int k = 0; k < V; ++k) r[c][k] = r[c][k] * p * (w[k] + a.w_off);
-    store_v<V>(a.h, t * a.h_ld + i, a.h_bf16, r[c]);
-  }
+  MOE_EACH(c, k) ss[0] = fmaf(r[c][k], r[c][k], ss[0]);
+  if (!KEEP) load_weight<V, NCH>(a.next_w, a.w_bf16, d, a.w_off, wn);
+  block_sum<1>(ss, red + 8, threads);
+  const float p = rsqrtf(fmaf(ss[0], a.inv_d, a.next_eps));
+  MOE_EACH(c, k) r[c][k] *= p * wn[c][k];
+  store_row<V, NCH>(a.h, t * a.h_ld, a.h_bf16, d, r);
+}
+
+// a(g) of a token gate, else 1
+__device__ __forceinline__ float token_gate(const void *gate, int kind, int act, int64_t i, int bf16) {
+  if (kind != MOE_GATE_TOKEN) return 1.f;
+  float g[1];
+  load_v<1>(gate, i, bf16, g);
+  return gate_value(g[0], act);
+}
+
+// One block per token, every load of the row on its way before the first sum.
+template <int V, int NCH>
+__global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd(const __grid_constant__ NormFwd a) {
+  __shared__ __align__(16) float red[16];
+  const int64_t t = blockIdx.x;
+  const int d = a.d;
+  float r[NCH][V], o[NCH][V], g[NCH][V], w[NCH][V], wn[NCH][V];
+  fill<V, NCH>(r, 0.f), fill<V, NCH>(o, 0.f), fill<V, NCH>(g, 0.f), fill<V, NCH>(w, 0.f), fill<V, NCH>(wn, 0.f);
+  load_row<V, NCH>(a.res, t * a.res_ld, a.res_bf16, d, r);
+  if (a.o) load_row<V, NCH>(a.o, t * a.o_ld, a.o_bf16, d, o);
+  if (gate_by_value(a.gate_kind))
+    load_row<V, NCH>(a.gate, a.gate_kind == MOE_GATE_FULL ? t * a.gate_ld : 0, a.gate_bf16, d, g);
+  const float gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+  constexpr bool KEEP = V * NCH <= 8;
+  if (KEEP && a.w) load_weight<V, NCH>(a.w, a.w_bf16, d, a.w_off, w);
+  if (KEEP && a.h) load_weight<V, NCH>(a.next_w, a.w_bf16, d, a.w_off, wn);
+  clear_sums(red);
+  fwd_row<V, NCH, KEEP>(a, t, r, o, g, w, wn, gt, red, blockDim.x, false);
 }
 
 struct NormBwd {
@@ -202,139 +277,326 @@ struct NormBwd {
   int64_t x_ld, dy_ld, gate_ld, dres_ld, dx_ld, dgate_ld;
   int x_bf16, dy_bf16, w_bf16, gate_bf16, dres_bf16, dx_bf16;
   int gate_kind, gate_act, d, n;
-  float eps, scale, w_off;
+  float eps, scale, w_off, inv_d;
 };
 
-// Persistent: block b takes rows b, b + grid, ...; the column sums stay in registers.
-template <int V, int NCH>
-__global__ void __launch_bounds__(kNormMaxThreads) k_norm_bwd(const __grid_constant__ NormBwd a) {
-  __shared__ float red[2][24];
-  const int d = a.d;
-  float dw[NCH][V], dg[NCH][V];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
-    for (int k = 0; k < V; ++k) dw[c][k] = dg[c][k] = 0.f;
-  const bool by_element = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
-  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
-    float x[NCH][V], dy[NCH][V];
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int i = (c * blockDim.x + threadIdx.x) * V;
-      if (i < d) {
-        load_v<V>(a.x, t * a.x_ld + i, a.x_bf16, x[c]);
-        load_v<V>(a.dy, t * a.dy_ld + i, a.dy_bf16, dy[c]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[c][k] = dy[c][k] = 0.f;
-      }
-    }
-    float gt = 1.f, gs = 0.f;  // token gate: its value, its slope
-    if (a.gate_kind == MOE_GATE_TOKEN) {
-      float g1[1];
-      load_v<1>(a.gate, t * a.gate_ld, a.gate_bf16, g1);
-      gt = gate_value(g1[0], a.gate_act);
-      gs = a.gate_act == MOE_GATE_SIGMOID ? gt * (1.f - gt) : 1.f;
-    }
-    // sums of x^2, of (dy a w) x and of dy x w (the token gate's gradient), without their common
-    // factors s and q
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int i = (c * blockDim.x + threadIdx.x) * V;
-      if (i >= d) continue;
-      float w[V], g[V];
-      if (a.w) load_v<V>(a.w, i, a.w_bf16, w);
-      if (by_element) load_v<V>(a.gate, (a.gate_kind == MOE_GATE_FULL ? t * a.gate_ld : 0) + i, a.gate_bf16, g);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float wk = a.w ? w[k] + a.w_off : 1.f;
-        const float av = by_element ? gate_value(g[k], a.gate_act) : gt;
-        const float e = dy[c][k] * x[c][k] * wk;
-        s[0] = fmaf(x[c][k], x[c][k], s[0]);
-        s[1] = fmaf(e, av, s[1]);
-        s[2] += e;
-      }
-    }
-    block_sum<3>(s, red[(t / gridDim.x) & 1]);
-    const float q = a.w ? rsqrtf(s[0] / d + a.eps) : 1.f;
-    const float m = a.w ? q * q * (s[1] / d) : 0.f;
-    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
-      float v1[1] = {a.scale * gs * q * s[2]};
-      store_v<1>(a.dgate, t * a.dgate_ld, a.gate_bf16, v1);
-    }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int i = (c * blockDim.x + threadIdx.x) * V;
-      if (i >= d) continue;
-      float w[V], g[V], out[V];
-      if (a.w) load_v<V>(a.w, i, a.w_bf16, w);
-      if (by_element) load_v<V>(a.gate, (a.gate_kind == MOE_GATE_FULL ? t * a.gate_ld : 0) + i, a.gate_bf16, g);
-      if (a.dres)
-        load_v<V>(a.dres, t * a.dres_ld + i, a.dres_bf16, out);
-      else
-#pragma unroll
-        for (int k = 0; k < V; ++k) out[k] = 0.f;
-      float gg[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float wk = a.w ? w[k] + a.w_off : 1.f;
-        const float av = by_element ? gate_value(g[k], a.gate_act) : gt;
-        const float dz = a.scale * dy[c][k];
-        out[k] = fmaf(q, dz * av * wk - a.scale * x[c][k] * m, out[k]);
-        dw[c][k] = fmaf(dz * av, x[c][k] * q, dw[c][k]);
-        const float slope = a.gate_act == MOE_GATE_SIGMOID ? av * (1.f - av) : 1.f;
-        gg[k] = dz * x[c][k] * q * wk * slope;
-        dg[c][k] += gg[k];
-      }
-      store_v<V>(a.dx, t * a.dx_ld + i, a.dx_bf16, out);
-      if (a.gate_kind == MOE_GATE_FULL && a.dgate) store_v<V>(a.dgate, t * a.dgate_ld + i, a.gate_bf16, gg);
+// What a block keeps from row to row: the sums over its rows, and (KEEP) the weight and a gate by column.
+template <int V, int NCH, bool KEEP>
+struct BwdState {
+  float dw[NCH][V], dg[NCH][V], w[NCH][V], gc[NCH][V];
+  __device__ __forceinline__ explicit BwdState(const NormBwd &a) {
+    fill<V, NCH>(dw, 0.f), fill<V, NCH>(dg, 0.f), fill<V, NCH>(w, a.w ? 0.f : 1.f), fill<V, NCH>(gc, 0.f);
+    if (KEEP) columns(a);
+  }
+  __device__ __forceinline__ void columns(const NormBwd &a) {
+    if (a.w) load_weight<V, NCH>(a.w, a.w_bf16, a.d, a.w_off, w);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      load_row<V, NCH>(a.gate, 0, a.gate_bf16, a.d, gc);
+      gate_values<V, NCH>(gc, a.gate_act);
     }
   }
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i = (c * blockDim.x + threadIdx.x) * V;
-    if (i >= d) continue;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * d + i;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (a.dw_part) a.dw_part[at + k] = dw[c][k];
-      if (a.dg_part) a.dg_part[at + k] = dg[c][k];
+  __device__ __forceinline__ void finish(const NormBwd &a) {
+    if (a.dw_part) store_row<V, NCH>(a.dw_part, static_cast<int64_t>(blockIdx.x) * a.d, 0, a.d, dw);
+    if (a.dg_part) store_row<V, NCH>(a.dg_part, static_cast<int64_t>(blockIdx.x) * a.d, 0, a.d, dg);
+  }
+};
+template <int V, int NCH>
+struct BwdRow {
+  float x[NCH][V], dy[NCH][V], dres[NCH][V], g[NCH][V];
+};
+
+template <int V, int NCH, bool KEEP>
+__device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, NCH> &q, BwdState<V, NCH, KEEP> &st, float gt,
+                                        float *red, int threads) {
+  const int d = a.d;
+  if (!KEEP) st.columns(a);
+  const bool channel = a.gate_kind == MOE_GATE_CHANNEL, full = a.gate_kind == MOE_GATE_FULL;
+  if (full) {
+    gate_values<V, NCH>(q.g, a.gate_act);
+  } else if (channel) {
+    MOE_EACH(c, k) q.g[c][k] = st.gc[c][k];
+  } else {
+    fill<V, NCH>(q.g, gt);
+  }
+  // sums of x^2, of (dy a w) x and of dy x w (the token gate's gradient), without their common
+  // factors s and q
+  float s[3] = {0.f, 0.f, 0.f};
+  MOE_EACH(c, k) {
+    const float e = q.dy[c][k] * q.x[c][k] * st.w[c][k];
+    s[0] = fmaf(q.x[c][k], q.x[c][k], s[0]);
+    s[1] = fmaf(e, q.g[c][k], s[1]);
+    s[2] += e;
+  }
+  block_sum<3>(s, red, threads);
+  const float root = a.w ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 1.f;
+  const float m = a.w ? a.scale * root * root * root * (s[1] * a.inv_d) : 0.f, sr = a.scale * root;
+  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID, want_dg = full || channel;
+  if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
+    float v1[1] = {(sigmoid ? gt * (1.f - gt) : 1.f) * sr * s[2]};
+    store_v<1>(a.dgate, t * a.dgate_ld, a.gate_bf16, v1);
+  }
+  // dx in dres, the gate's gradient in g
+  MOE_EACH(c, k) {
+    const float x = q.x[c][k], av = q.g[c][k], sdy = sr * q.dy[c][k], da = sdy * av;
+    q.dres[c][k] = fmaf(da, st.w[c][k], fmaf(-m, x, q.dres[c][k]));
+    st.dw[c][k] = fmaf(da, x, st.dw[c][k]);
+    if (want_dg) {
+      const float gg = sdy * x * st.w[c][k] * (sigmoid ? av - av * av : 1.f);
+      st.dg[c][k] += gg;
+      q.g[c][k] = gg;
     }
+  }
+  store_row<V, NCH>(a.dx, t * a.dx_ld, a.dx_bf16, d, q.dres);
+  if (full && a.dgate) store_row<V, NCH>(a.dgate, t * a.dgate_ld, a.gate_bf16, d, q.g);
+}
+
+// Persistent: block b takes rows b, b + grid, ...; where a thread holds few values of a row (NEXT) the
+// next row is loaded while this one is summed (without it, a row took 6 us of latency after latency:
+// 28 us for 4 rows a block).
+template <int V, int NCH>
+__global__ void __launch_bounds__(kNormMaxThreads) k_norm_bwd(const __grid_constant__ NormBwd a) {
+  constexpr bool NEXT = V * NCH <= 8;
+  __shared__ __align__(16) float red[48];
+  const int d = a.d, threads = blockDim.x;
+  clear_sums(red);
+  constexpr bool KEEP = V * NCH <= 16;
+  BwdState<V, NCH, KEEP> st(a);
+  auto load = [&](int64_t t, BwdRow<V, NCH> &q, float &gt) {
+    fill<V, NCH>(q.x, 0.f), fill<V, NCH>(q.dy, 0.f), fill<V, NCH>(q.dres, 0.f), fill<V, NCH>(q.g, 0.f);
+    if (t >= a.n) return;
+    load_row<V, NCH>(a.x, t * a.x_ld, a.x_bf16, d, q.x);
+    load_row<V, NCH>(a.dy, t * a.dy_ld, a.dy_bf16, d, q.dy);
+    if (a.dres) load_row<V, NCH>(a.dres, t * a.dres_ld, a.dres_bf16, d, q.dres);
+    if (a.gate_kind == MOE_GATE_FULL) load_row<V, NCH>(a.gate, t * a.gate_ld, a.gate_bf16, d, q.g);
+    gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+  };
+  if (NEXT) {
+    BwdRow<V, NCH> q0, q1;
+    float g0 = 1.f, g1 = 1.f;
+    load(blockIdx.x, q0, g0);
+    for (int64_t t = blockIdx.x; t < a.n; t += 2 * gridDim.x) {
+      load(t + gridDim.x, q1, g1);
+      bwd_row<V, NCH, KEEP>(a, t, q0, st, g0, red, threads);
+      if (t + gridDim.x >= a.n) break;
+      load(t + 2 * gridDim.x, q0, g0);
+      bwd_row<V, NCH, KEEP>(a, t + gridDim.x, q1, st, g1, red + 24, threads);
+    }
+  } else {
+    int k = 0;
+    for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x, k ^= 1) {
+      BwdRow<V, NCH> q;
+      float gt = 1.f;
+      load(t, q, gt);
+      bwd_row<V, NCH, KEEP>(a, t, q, st, gt, red + 24 * k, threads);
+    }
+  }
+  st.finish(a);
+}
+
+// ------------------------------------------------------------------------------------------
+// Many rows of whole vectors: persistent blocks fed by a ring of bulk copies.  A stage holds the rows
+// of one token that the kernel reads (contiguous runs of d values, 16-byte aligned); the block's last
+// warp refills a stage when the others have its values in registers, so the copies of the next rows
+// never wait for a row's sums, and a row costs its arithmetic, not its latencies.
+// ------------------------------------------------------------------------------------------
+__device__ uint32_t g_norm_err;  // a bounded wait ran out
+constexpr uint64_t kNormSpin = 2000000000ull;
+constexpr int kRingMaxStages = 6, kRingMaxRows = 4;
+
+struct RowSource {
+  const void *p;
+  int64_t ld;
+  int bf16;
+};
+struct Ring {
+  RowSource src[kRingMaxRows];
+  int n_src, stages, stage_bytes;
+};
+
+struct RingState {
+  unsigned char *base;
+  uint64_t *full, *empty;
+  uint64_t limit;
+  int threads;  // that compute: all warps but the last
+  __device__ RingState(unsigned char *smem, const Ring &r) : base(smem + 128), limit(kNormSpin), threads(blockDim.x - 32) {
+    full = reinterpret_cast<uint64_t *>(smem);
+    empty = full + kRingMaxStages;
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < r.stages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], threads / 32);
+      }
+      fence_barrier_init();
+    }
+  }
+  __device__ bool producer() const { return static_cast<int>(threadIdx.x) >= threads; }
+  // The last warp: lane i copies row i of a token, k-th token of this block after the other.  A wait
+  // that runs out ends it: the others then find no data, see wait().
+  __device__ void produce(const Ring &r, int d, int n) const {
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane < r.n_src;
+    const RowSource src = r.src[mine ? lane : 0];
+    const int size = src.bf16 ? 2 : 4;
+    int off = 0;
+    for (int i = 0; i < lane && i < r.n_src; ++i) off += d * (r.src[i].bf16 ? 2 : 4);
+    const char *p = static_cast<const char *>(src.p) + blockIdx.x * src.ld * size;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * src.ld * size;
+    int s = 0, phase = 1;
+    for (int64_t t = blockIdx.x; t < n; t += gridDim.x) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, kNormSpin))) {
+        if (lane == 0) flag_error(&g_norm_err, kErrTimeout);
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], r.stage_bytes);
+      __syncwarp();
+      if (mine) bulk_g2s(base + s * r.stage_bytes + off, p, d * size, &full[s]);
+      p += step;
+      if (++s == r.stages) s = 0, phase ^= 1;
+    }
+    // nothing may be on its way when the block leaves: the others have waited for every full stage, or
+    // given up; then wait here
+    __syncwarp();
+  }
+  // A thread whose wait ran out sets the error word and does not wait again: what it then reads and
+  // writes is in bounds, and every barrier is still reached.
+  __device__ __forceinline__ const unsigned char *wait(const Ring &r, int s, int phase) {
+    if (!mbar_wait_bounded(&full[s], phase, limit)) {
+      limit = 0;
+      flag_error(&g_norm_err, kErrTimeout);
+    }
+    return base + s * r.stage_bytes;
+  }
+  __device__ __forceinline__ void release(int s) const {  // this warp has the stage in registers
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
+  }
+};
+
+constexpr int kRingThreads = kNormMaxThreads + 32;
+
+template <int NCH>
+__global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 3 : NCH == 2 ? 2 : 1) k_norm_fwd_ring(const __grid_constant__ NormFwd a,
+                                                                                 const __grid_constant__ Ring r, int n) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(16) float red[32];
+  constexpr int V = 8;
+  const int d = a.d;
+  RingState ring(smem, r);
+  clear_sums(red);
+  if (ring.producer()) {
+    ring.produce(r, d, n);
+    return;
+  }
+  // in registers for a block's rows while they are few; from L1 where that would cost a block of the SM
+  constexpr bool KEEP = NCH == 1;
+  float w[NCH][V], wn[NCH][V], gc[NCH][V];
+  fill<V, NCH>(w, 0.f), fill<V, NCH>(wn, 0.f), fill<V, NCH>(gc, 0.f);
+  const bool full = a.gate_kind == MOE_GATE_FULL, channel = a.gate_kind == MOE_GATE_CHANNEL;
+  if (KEEP) {
+    if (a.w) load_weight<V, NCH>(a.w, a.w_bf16, d, a.w_off, w);
+    if (a.h) load_weight<V, NCH>(a.next_w, a.w_bf16, d, a.w_off, wn);
+    if (channel) {
+      load_row<V, NCH>(a.gate, 0, a.gate_bf16, d, gc);
+      gate_values<V, NCH>(gc, a.gate_act);
+    }
+  }
+  int s = 0, phase = 0, turn = 0;
+  for (int64_t t = blockIdx.x; t < n; t += gridDim.x, turn ^= 16) {
+    float x[NCH][V], o[NCH][V], g[NCH][V];
+    fill<V, NCH>(x, 0.f), fill<V, NCH>(o, 0.f), fill<V, NCH>(g, 0.f);
+    const float gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+    const unsigned char *p = ring.wait(r, s, phase);
+    load_row<V, NCH>(p, 0, a.res_bf16, d, x);
+    p += d * (a.res_bf16 ? 2 : 4);
+    if (a.o) {
+      load_row<V, NCH>(p, 0, a.o_bf16, d, o);
+      p += d * (a.o_bf16 ? 2 : 4);
+      if (full)
+        load_row<V, NCH>(p, 0, a.gate_bf16, d, g);
+      else if (!KEEP && channel)
+        load_row<V, NCH>(a.gate, 0, a.gate_bf16, d, g);
+      else
+        MOE_EACH(c, i) g[c][i] = gc[c][i];
+    }
+    ring.release(s);
+    if (++s == r.stages) s = 0, phase ^= 1;
+    fwd_row<V, NCH, KEEP>(a, t, x, o, g, w, wn, gt, red + turn, ring.threads, KEEP && channel);
   }
 }
 
-// out[i] = sum over rows of part[row][i], in row order within eight interleaved runs that are then
-// added in order; blockIdx.y picks one of two sums.
+template <int NCH>
+__global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 2 : 1) k_norm_bwd_ring(const __grid_constant__ NormBwd a,
+                                                                                 const __grid_constant__ Ring r) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(16) float red[48];
+  constexpr int V = 8;
+  const int d = a.d;
+  RingState ring(smem, r);
+  clear_sums(red);
+  if (ring.producer()) {
+    ring.produce(r, d, a.n);
+    return;
+  }
+  constexpr bool KEEP = NCH == 1;
+  BwdState<V, NCH, KEEP> st(a);
+  int s = 0, phase = 0, turn = 0;
+  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x, turn ^= 1) {
+    BwdRow<V, NCH> q;
+    fill<V, NCH>(q.x, 0.f), fill<V, NCH>(q.dy, 0.f), fill<V, NCH>(q.dres, 0.f), fill<V, NCH>(q.g, 0.f);
+    const float gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+    const unsigned char *p = ring.wait(r, s, phase);
+    load_row<V, NCH>(p, 0, a.x_bf16, d, q.x);
+    p += d * (a.x_bf16 ? 2 : 4);
+    load_row<V, NCH>(p, 0, a.dy_bf16, d, q.dy);
+    p += d * (a.dy_bf16 ? 2 : 4);
+    if (a.dres) {
+      load_row<V, NCH>(p, 0, a.dres_bf16, d, q.dres);
+      p += d * (a.dres_bf16 ? 2 : 4);
+    }
+    if (a.gate_kind == MOE_GATE_FULL) load_row<V, NCH>(p, 0, a.gate_bf16, d, q.g);
+    ring.release(s);
+    if (++s == r.stages) s = 0, phase ^= 1;
+    bwd_row<V, NCH, KEEP>(a, t, q, st, gt, red + 24 * turn, ring.threads);
+  }
+  st.finish(a);
+}
+
+// out[i] = sum over rows of part[row][i]: 32 threads a column add every 32nd row in order, their sums
+// are added in order; blockIdx.y picks one of two sums.
 struct ColSum {
   const float *part[2];
   void *out[2];
   int bf16[2];
   int rows, d;
 };
-__global__ void __launch_bounds__(256) k_colsum(ColSum a) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) k_colsum(ColSum a) {
+  __shared__ float s[32][33];
   const int which = blockIdx.y, i = blockIdx.x * 32 + threadIdx.x;
-  const float *part = a.part[which];
+  const float *part = a.part[which] + i;
   float v = 0.f;
-  if (i < a.d)
-    for (int r = threadIdx.y; r < a.rows; r += 8) v += part[static_cast<int64_t>(r) * a.d + i];
+  if (i < a.d) {
+#pragma unroll 8
+    for (int r = threadIdx.y; r < a.rows; r += 32) v += part[static_cast<int64_t>(r) * a.d];
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y == 0 && i < a.d) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+    for (int k = 1; k < 32; ++k) v += s[k][threadIdx.x];
     float o[1] = {v};
     store_v<1>(a.out[which], i, a.bf16[which], o);
   }
 }
 
-// Rows can be read 8 values at a time: every pointer and row stride a multiple of 16 bytes.
+// Values that can be read and written at once: the width, and every pointer and row stride, a
+// multiple of v values.
 struct VecRule {
-  bool ok;
-  explicit VecRule(int d) : ok(d % 8 == 0) {}
+  int v;
+  explicit VecRule(int d) : v(d % 8 == 0 ? 8 : d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1) {}
   void row(const void *p, int64_t ld, int bf16) {
-    if (p) ok = ok && aligned16(p) && (ld * (bf16 ? 2 : 4)) % 16 == 0;
+    const int size = bf16 ? 2 : 4;
+    if (p)
+      while (v > 1 && (reinterpret_cast<uintptr_t>(p) % (v * size > 16 ? 16 : v * size) || ld % v)) v /= 2;
   }
 };
 
@@ -343,15 +605,19 @@ int norm_threads(int d, int v) {
   return t < kNormMaxThreads ? t : kNormMaxThreads;
 }
 
-// Calls f with the instantiation that holds a row of d values.
+// Calls f with the instantiation that holds a row of d <= kNormMaxD values, v at a time.
 template <typename F>
-cudaError_t pick_norm(int d, bool vec, F f) {
-  const int v = vec ? 8 : 1, threads = norm_threads(d, v), nch = (d + v * threads - 1) / (v * threads);
+cudaError_t pick_norm(int d, int v, F f) {
+  const int threads = norm_threads(d, v), nch = (d + v * threads - 1) / (v * threads);
 #define MOE_NORM_CASE(V, N) f(std::integral_constant<int, V>{}, std::integral_constant<int, N>{}, threads)
-  if (vec)
+  if (v == 8)
     nch <= 1 ? MOE_NORM_CASE(8, 1) : nch <= 2 ? MOE_NORM_CASE(8, 2) : MOE_NORM_CASE(8, 4);
+  else if (v == 4)
+    nch <= 1 ? MOE_NORM_CASE(4, 1) : nch <= 2 ? MOE_NORM_CASE(4, 2) : nch <= 4 ? MOE_NORM_CASE(4, 4) : MOE_NORM_CASE(4, 8);
+  else if (v == 2)
+    nch <= 2 ? MOE_NORM_CASE(2, 2) : nch <= 4 ? MOE_NORM_CASE(2, 4) : nch <= 8 ? MOE_NORM_CASE(2, 8) : MOE_NORM_CASE(2, 16);
   else
-    nch <= 1 ? MOE_NORM_CASE(1, 1) : nch <= 4 ? MOE_NORM_CASE(1, 4) : nch <= 8 ? MOE_NORM_CASE(1, 8)
+    nch <= 2 ? MOE_NORM_CASE(1, 2) : nch <= 4 ? MOE_NORM_CASE(1, 4) : nch <= 8 ? MOE_NORM_CASE(1, 8)
                                    : nch <= 16 ? MOE_NORM_CASE(1, 16) : MOE_NORM_CASE(1, 32);
 #undef MOE_NORM_CASE
   return cudaGetLastError();
@@ -375,16 +641,86 @@ moe_status check_gate(const void *gate, int kind, int act, int dt, int64_t ld, i
   return MOE_OK;
 }
 
-moe_status launch_fwd(const NormFwd &a, int n, bool vec, cudaStream_t st) {
-  const cudaError_t e = pick_norm(a.d, vec, [&](auto v, auto nch, int threads) {
-    k_norm_fwd<decltype(v)::value, decltype(nch)::value><<<n, threads, 0, st>>>(a);
-  });
+// The ring of a kernel over n rows, or stages = 0 where it does not pay: rows that are not whole
+// 16-byte vectors, too long for two stages, or (backward) for the registers, or fewer than kRingRows
+// for each of the blocks that fill the device (1,180 x 2,048, fp32: 12.5 us against 10.5; 8,192 x
+// 4,096, bf16 with a gate of its own: 57 against 97).
+constexpr int kRingBytes = 208 * 1024, kRingRows = 4, kMostBlocksPerSm = 16;
+struct RingPlan {
+  Ring r{};
+  int blocks = 0, threads = 0, smem = 0;
+  cudaError_t err = cudaSuccess;
+  RingPlan(std::initializer_list<RowSource> src, int n, int d, int v, bool backward) {
+    if (v != 8) return;
+    for (const RowSource &s : src)
+      if (s.p) r.src[r.n_src++] = s, r.stage_bytes += d * (s.bf16 ? 2 : 4);
+    int nsm = 0;
+    if ((err = current_sm_count(&nsm)) != cudaSuccess) return;
+    threads = norm_threads(d, v);
+    // as many blocks as the registers hold (72 a thread forward, 96 backward, all of them beyond), of at
+    // least three stages each
+    int per_sm = kRingBytes / (3 * r.stage_bytes);
+    const int wide = d > 8 * kNormMaxThreads;
+    const int most = wide ? (backward || d > 16 * kNormMaxThreads ? 1 : 2) : 65536 / ((backward ? 96 : 72) * (threads + 32));
+    per_sm = per_sm > most ? most : per_sm;
+    per_sm = per_sm > kMostBlocksPerSm ? kMostBlocksPerSm : per_sm < 1 ? 1 : per_sm;
+    if (n < kRingRows * nsm * (per_sm < 3 ? per_sm : 3) || (backward && d > 16 * kNormMaxThreads)) return;
+    if (per_sm > n / (kRingRows * nsm)) per_sm = n / (kRingRows * nsm);
+    int stages = (kRingBytes / per_sm - 1024) / r.stage_bytes;
+    if (stages > kRingMaxStages) stages = kRingMaxStages;
+    blocks = per_sm * nsm;
+    smem = 128 + stages * r.stage_bytes;
+    if (stages >= 2) r.stages = stages;
+  }
+};
+
+template <int MOST, typename F>
+cudaError_t pick_ring(int d, F f) {
+  const int nch = (d + 8 * kNormMaxThreads - 1) / (8 * kNormMaxThreads);
+  if (nch <= 1)
+    f(std::integral_constant<int, 1>{});
+  else if (nch <= 2)
+    f(std::integral_constant<int, 2>{});
+  else if constexpr (MOST == 4)
+    f(std::integral_constant<int, 4>{});
+  return cudaGetLastError();
+}
+
+// Once per device, with it current.
+cudaError_t configure_rings() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kMaxDevices && done[dev].load(std::memory_order_acquire))) return e;
+  const void *ks[] = {(const void *)k_norm_fwd_ring<1>, (const void *)k_norm_fwd_ring<2>, (const void *)k_norm_fwd_ring<4>,
+                      (const void *)k_norm_bwd_ring<1>, (const void *)k_norm_bwd_ring<2>};
+  for (const void *k : ks)
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)) != cudaSuccess) return e;
+  if (dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
+moe_status launch_fwd(const NormFwd &a, int n, int v, cudaStream_t st) {
+  const bool full = a.gate_kind == MOE_GATE_FULL;
+  const RingPlan p({{a.res, a.res_ld, a.res_bf16}, {a.o, a.o_ld, a.o_bf16}, {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, n,
+                   a.d, v, false);
+  cudaError_t e = p.err;
+  if (e == cudaSuccess && p.r.stages) {
+    e = configure_rings();
+    if (e == cudaSuccess)
+      e = pick_ring<4>(a.d, [&](auto nch) { k_norm_fwd_ring<decltype(nch)::value><<<p.blocks, p.threads + 32, p.smem, st>>>(a, p.r, n); });
+  } else if (e == cudaSuccess) {
+    e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
+      k_norm_fwd<decltype(vv)::value, decltype(nch)::value><<<n, threads, 0, st>>>(a);
+    });
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Blocks of the backward grid: enough to fill the device, no more than rows; the partial sums need
 // one row of d values for each.
-constexpr int kBwdBlocksPerSm = 2;
+constexpr int kBwdBlocksPerSm = 3;
 cudaError_t bwd_blocks(int n, int *blocks) {
   int nsm = 0;
   const cudaError_t e = current_sm_count(&nsm);
@@ -392,13 +728,15 @@ cudaError_t bwd_blocks(int n, int *blocks) {
   return e;
 }
 
-moe_status run_bwd(NormBwd &a, bool vec, void *dw, int dw_bf16, void *dg, int dg_bf16, void *ws, uint64_t ws_bytes,
+moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf16, void *ws, uint64_t ws_bytes,
                    cudaStream_t st) {
-  int blocks = 0;
-  if (bwd_blocks(a.n, &blocks) != cudaSuccess) return MOE_ERR_CUDA;
+  const bool full = a.gate_kind == MOE_GATE_FULL;
+  const RingPlan p({{a.x, a.x_ld, a.x_bf16}, {a.dy, a.dy_ld, a.dy_bf16}, {a.dres, a.dres_ld, a.dres_bf16},
+                    {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, a.n, a.d, v, true);
+  int blocks = p.blocks;
+  if (p.err != cudaSuccess || (!p.r.stages && bwd_blocks(a.n, &blocks) != cudaSuccess)) return MOE_ERR_CUDA;
   const int sums = (dw ? 1 : 0) + (dg ? 1 : 0);
-  const uint64_t need = static_cast<uint64_t>(blocks) * a.d * 4;
-  if (sums && (!ws || ws_bytes < need * sums || !aligned16(ws))) return MOE_ERR_INVALID_ARGUMENT;
+  if (sums && (!ws || ws_bytes < moe_norm_workspace(a.n, a.d) || !aligned16(ws))) return MOE_ERR_INVALID_ARGUMENT;
   float *part = static_cast<float *>(ws);
   ColSum c{};
   c.rows = blocks;
@@ -413,11 +751,18 @@ moe_status run_bwd(NormBwd &a, bool vec, void *dw, int dw_bf16, void *dg, int dg
     a.dg_part = part;
     c.part[k] = part, c.out[k] = dg, c.bf16[k] = dg_bf16, ++k;
   }
-  cudaError_t e = pick_norm(a.d, vec, [&](auto v, auto nch, int threads) {
-    k_norm_bwd<decltype(v)::value, decltype(nch)::value><<<blocks, threads, 0, st>>>(a);
-  });
+  cudaError_t e;
+  if (p.r.stages) {
+    e = configure_rings();
+    if (e == cudaSuccess)
+      e = pick_ring<2>(a.d, [&](auto nch) { k_norm_bwd_ring<decltype(nch)::value><<<p.blocks, p.threads + 32, p.smem, st>>>(a, p.r); });
+  } else {
+    e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
+      k_norm_bwd<decltype(vv)::value, decltype(nch)::value><<<blocks, threads, 0, st>>>(a);
+    });
+  }
   if (e == cudaSuccess && sums) {
-    k_colsum<<<dim3((a.d + 31) / 32, sums), dim3(32, 8), 0, st>>>(c);
+    k_colsum<<<dim3((a.d + 31) / 32, sums), dim3(32, 32), 0, st>>>(c);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -427,6 +772,17 @@ moe_status run_bwd(NormBwd &a, bool vec, void *dw, int dw_bf16, void *dg, int dg
 }  // namespace moe
 
 using namespace moe;
+
+namespace moe {
+cudaError_t take_norm_error(uint32_t *err) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_err, sizeof v);
+  *err = v;
+  if (e != cudaSuccess || !v) return e;
+  v = 0;
+  return cudaMemcpyToSymbol(g_norm_err, &v, sizeof v);
+}
+}  // namespace moe
 
 extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype,
                                   float eps, int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride,
@@ -440,10 +796,10 @@ extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stri
   a.res = x, a.res_ld = x_stride, a.res_bf16 = x_dtype == MOE_BF16;
   a.next_w = weight, a.w_bf16 = w_dtype == MOE_BF16, a.next_eps = eps, a.w_off = static_cast<float>(unit_offset);
   a.h = h, a.h_ld = h_stride, a.h_bf16 = h_dtype == MOE_BF16;
-  a.d = d_model;
+  a.d = d_model, a.inv_d = 1.f / d_model;
   VecRule v(d_model);
-  v.row(x, x_stride, a.res_bf16), v.row(h, h_stride, a.h_bf16), v.row(weight, 0, 0);
-  return launch_fwd(a, n_tokens, v.ok, static_cast<cudaStream_t>(stream));
+  v.row(x, x_stride, a.res_bf16), v.row(h, h_stride, a.h_bf16), v.row(weight, 0, a.w_bf16);
+  return launch_fwd(a, n_tokens, v.v, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status moe_norm_out(const moe_norm_out_args *p, void *stream) {
@@ -468,22 +824,24 @@ extern "C" moe_status moe_norm_out(const moe_norm_out_args *p, void *stream) {
   a.res_out = p->res_out, a.out_ld = p->res_out_stride, a.out_bf16 = p->res_out_dtype == MOE_BF16;
   a.next_w = p->next_weight, a.next_eps = p->next_eps;
   a.h = p->h, a.h_ld = p->h_stride, a.h_bf16 = p->h_dtype == MOE_BF16;
-  a.d = d;
+  a.d = d, a.inv_d = 1.f / d;
   VecRule v(d);
   v.row(a.o, a.o_ld, a.o_bf16), v.row(a.res, a.res_ld, a.res_bf16), v.row(a.res_out, a.out_ld, a.out_bf16);
-  v.row(a.h, a.h_ld, a.h_bf16), v.row(a.w, 0, 0), v.row(a.next_w, 0, 0);
+  v.row(a.h, a.h_ld, a.h_bf16), v.row(a.w, 0, a.w_bf16), v.row(a.next_w, 0, a.w_bf16);
   if (a.gate_kind == MOE_GATE_FULL) v.row(a.gate, a.gate_ld, a.gate_bf16);
-  if (a.gate_kind == MOE_GATE_CHANNEL) v.row(a.gate, 0, 0);
-  return launch_fwd(a, n, v.ok, static_cast<cudaStream_t>(stream));
+  if (a.gate_kind == MOE_GATE_CHANNEL) v.row(a.gate, 0, a.gate_bf16);
+  return launch_fwd(a, n, v.v, static_cast<cudaStream_t>(stream));
 }
 
+// Two sums of a row of d values for every block that a backward grid can have.
 extern "C" uint64_t moe_norm_workspace(int32_t n_tokens, int32_t d_model) {
-  int blocks = 0;
-  if (n_tokens < 1 || d_model < 1 || d_model > kNormMaxD || bwd_blocks(n_tokens, &blocks) != cudaSuccess) {
+  int nsm = 0;
+  if (n_tokens < 1 || d_model < 1 || d_model > kNormMaxD || current_sm_count(&nsm) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  return static_cast<uint64_t>(blocks) * d_model * 8;
+  const int64_t most = static_cast<int64_t>(nsm) * (d_model >= 2048 ? 3 : kMostBlocksPerSm);
+  return static_cast<uint64_t>(n_tokens < most ? n_tokens : most) * d_model * 8;
 }
 
 extern "C" moe_status moe_norm_in_backward(const moe_norm_in_bwd_args *p, void *stream) {
@@ -501,11 +859,11 @@ extern "C" moe_status moe_norm_in_backward(const moe_norm_in_bwd_args *p, void *
   a.w = p->weight, a.w_bf16 = p->w_dtype == MOE_BF16, a.w_off = static_cast<float>(p->unit_offset), a.eps = p->eps;
   a.dres = p->dres, a.dres_ld = p->dres_stride, a.dres_bf16 = p->dres_dtype == MOE_BF16;
   a.dx = p->dx, a.dx_ld = p->dx_stride, a.dx_bf16 = p->dx_dtype == MOE_BF16;
-  a.gate_kind = MOE_GATE_NONE, a.scale = 1.f, a.d = d, a.n = n;
+  a.gate_kind = MOE_GATE_NONE, a.scale = 1.f, a.d = d, a.n = n, a.inv_d = 1.f / d;
   VecRule v(d);
   v.row(a.x, a.x_ld, a.x_bf16), v.row(a.dy, a.dy_ld, a.dy_bf16), v.row(a.dres, a.dres_ld, a.dres_bf16);
-  v.row(a.dx, a.dx_ld, a.dx_bf16), v.row(a.w, 0, 0);
-  return run_bwd(a, v.ok, p->dweight, a.w_bf16, nullptr, 0, p->workspace, p->workspace_bytes,
+  v.row(a.dx, a.dx_ld, a.dx_bf16), v.row(a.w, 0, a.w_bf16);
+  return run_bwd(a, v.v, p->dweight, a.w_bf16, nullptr, 0, p->workspace, p->workspace_bytes,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -531,11 +889,11 @@ extern "C" moe_status moe_norm_out_backward(const moe_norm_out_bwd_args *p, void
   a.dx = p->d_o, a.dx_ld = p->do_stride, a.dx_bf16 = a.x_bf16;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (!channel) a.dgate = p->dgate, a.dgate_ld = p->dgate_stride;
-  a.scale = p->scale, a.d = d, a.n = n;
+  a.scale = p->scale, a.d = d, a.n = n, a.inv_d = 1.f / d;
   VecRule v(d);
-  v.row(a.x, a.x_ld, a.x_bf16), v.row(a.dy, a.dy_ld, a.dy_bf16), v.row(a.dx, a.dx_ld, a.dx_bf16), v.row(a.w, 0, 0);
+  v.row(a.x, a.x_ld, a.x_bf16), v.row(a.dy, a.dy_ld, a.dy_bf16), v.row(a.dx, a.dx_ld, a.dx_bf16), v.row(a.w, 0, a.w_bf16);
   if (a.gate_kind == MOE_GATE_FULL) v.row(a.gate, a.gate_ld, a.gate_bf16), v.row(a.dgate, a.dgate_ld, a.gate_bf16);
-  if (channel) v.row(a.gate, 0, 0);
-  return run_bwd(a, v.ok, p->dweight, a.w_bf16, channel ? p->dgate : nullptr, a.gate_bf16, p->workspace,
+  if (channel) v.row(a.gate, 0, a.gate_bf16);
+  return run_bwd(a, v.v, p->dweight, a.w_bf16, channel ? p->dgate : nullptr, a.gate_bf16, p->workspace,
                  p->workspace_bytes, static_cast<cudaStream_t>(stream));
 }

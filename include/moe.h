@@ -200,6 +200,10 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
  * Outputs may not overlap inputs unless said so.
  * ------------------------------------------------------------------------------------------- */
+/* Waits for the current device and returns (and clears) a pending MOE_ERR_TIMEOUT of the norms' and
+ * the dense block's kernels there: a bounded wait ran out and the results of a call are not valid. */
+moe_status moe_block_check(void);
+
 /* What a gate is broadcast over: one value per column, per token, or of its own for every value. */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
 /* a(g) = g, or sigmoid(g) */
@@ -340,10 +344,6 @@ typedef struct {
   int64_t dy_stride, x_stride, dx_stride;
 } moe_ffn_bwd_args;
 moe_status moe_ffn_backward(const moe_ffn_bwd_args *args, void *stream);
-/* Synchronises the current device and returns (and clears) a pending MOE_ERR_TIMEOUT of the dense
- * block's kernels there: a bounded wait ran out and the call's results are not valid. */
-moe_status moe_ffn_check(void);
-
 /* A run of layers first_layer .. first_layer + n_layers - 1 with everything that stands around and
  * beside their routed experts, x kept in fp32 between the layers:
  *   a = norm_in(x)            o = MoE_l(a) (+ dense block(a)) (+ adapters(a))

@@ -13,7 +13,7 @@ def P():
     import expert_ffn_gemv_b200 as P
 
     yield P
-    assert P.ffn_check() == P.MOE_OK  # no wait ran out
+    assert P.block_check() == P.MOE_OK  # no wait ran out
 
 
 def randn(*shape, seed, std=1.0, dtype=BF):

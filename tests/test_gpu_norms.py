@@ -156,6 +156,40 @@ def test_norm_out_backward(P, gate, act, n, d, ot, rt):
                     R.near(v, r, size * 2 * R.NORM + r.abs() * R.HALF[t], name)
 
 
+@pytest.mark.parametrize("n,d,ot,rt,gate", [(592, 8, F, F, "full"), (2000, 264, BF, F, "token"), (5000, 1000, F, BF, "full"),
+                                            (1500, 2048, F, F, "channel"), (2500, 4096, BF, BF, "full"), (600, 8192, F, F, "none"),
+                                            (600, 8192, F, F, "full"), (8192, 32, BF, BF, "channel"), (700, 5000, BF, F, "full")])
+def test_many_rows(P, n, d, ot, rt, gate):
+    """The sizes at which blocks walk over rows, strided and not."""
+    wide = randn(n, d + 8, seed=1, std=0.5, dtype=ot)
+    res, dres, dh = randn(n, d, seed=2, std=2.0, dtype=rt), randn(n, d, seed=5, std=0.1, dtype=rt), randn(n, d, seed=6, std=0.1, dtype=BF)
+    w, wn, g = randn(d, seed=3, std=0.3, mean=1.0), randn(d, seed=4, std=0.3, mean=1.0), gate_of(gate, n, d, BF)
+    kw = dict(weight=w, eps=R.EPS, gate=g, gate_act="sigmoid", scale=0.7)
+    for o in (wide[:, 8:], wide[:, 8:].contiguous()):
+        out, h = P.norm_out(o, res, next_weight=wn, next_eps=R.EPS, next_dtype=BF, **kw)
+        ref, term = R.norm_out(o, res, w, g, "sigmoid", 0.7)
+        R.near(out, ref, term * R.NORM + ref.abs() * (2.0 ** -23 + R.HALF[rt]), "res")
+        href = R.norm_in(out, wn)
+        R.near(h, href, href.abs() * (R.NORM + R.HALF[BF]), "h")
+        assert torch.equal(h, P.norm_in(out, wn, eps=R.EPS, out_dtype=BF))
+        dx, dwn = P.norm_in_backward(out, wn, dh, eps=R.EPS, d_residual=dres)
+        rx, rw, sx, sw = R.norm_in_backward(out, wn, dh, dres)
+        R.near(dx, rx, sx * R.NORM + rx.abs() * R.HALF[rt], "dx")
+        R.near(dwn, rw, sw * 2 * R.NORM + rw.abs() * R.HALF[F], "dwn")
+        got = P.norm_out_backward(o, dres, **kw)
+        want = R.norm_out_backward(o, dres, w, g, "sigmoid", 0.7)
+        for v, name, t in zip(got, ("d_o", "d_w", "d_gate"), (ot, F, BF)):
+            if v is not None:
+                r, size = want[name]
+                R.near(v, r, size * 2 * R.NORM + r.abs() * R.HALF[t], name)
+        again = P.norm_out_backward(o, dres, **kw)
+        assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
+    few = P.norm_out(wide[:9, 8:], res[:9], next_weight=wn, next_eps=R.EPS, next_dtype=BF,
+                     **{**kw, "gate": g[:9] if gate in ("token", "full") else g})
+    assert torch.equal(few[0], out[:9]) and torch.equal(few[1], h[:9])  # a row does not depend on their number
+    assert P.block_check() == P.MOE_OK
+
+
 def test_gradients_against_differences(P):
     """Of the kernels' own forward: sum(dres * res_out) + sum(dh * h) along a direction.  The values are
     of order 1, n d = 4096 of them: an fp32 result is 2^-23 off, so the difference over 2 e is off by
