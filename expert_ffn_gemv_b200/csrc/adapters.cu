@@ -4,10 +4,17 @@
 //
 // The tokens are grouped by adapter into tiles of at most TM tokens of one adapter; a cluster of CL
 // blocks runs both products of a tile in one kernel: block c takes a slice of d_in for
-// v = A_i x (mma.sync, warps on interleaved 32-column pieces, the x rows read from global memory
-// straight into the operand registers), the blocks' partial v meet over distributed shared memory
-// and are added in block order, then block c multiplies its slice of d_out by v and adds the base.
-// So x, base and out cross HBM once and v never leaves the SMs.
+// v = A_i x (mma.sync), the blocks' partial v meet over distributed shared memory and are added in
+// block order, then block c multiplies its slice of d_out by v and adds the base.  So x, base and out
+// cross HBM once and v never leaves the SMs.  A warp has 16 of the tile's tokens (TM / 16 groups of
+// warps, whose equal weight loads meet in L1) and every KG-th 32-deep piece.
+//
+// What bounds it is latency: a piece is a few MMAs behind its loads.  So everything comes through
+// rings in shared memory, several pieces ahead: x and base by cp.async, in which every lane copies just
+// the 16-byte words that it takes out itself (no barrier: a thread waits for its own groups), and the
+// weights, packed in operand order, by bulk copies of the block's ninth warp, one ring for the warps
+// that share them.  (8,192 tokens, 2,048 -> 4,096, rank 64: with weights loaded one piece ahead into
+// registers a piece took 1.6 us.)
 //
 // Precision: products of bf16 values with fp32 accumulators.  What is not bf16 by itself (fp32 x, and
 // v between the two products) enters as bf16 parts that add up to it: two where out is bf16 (2^-16 of
@@ -21,7 +28,8 @@ using namespace moe;
 
 namespace {
 
-constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;
+constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;  // that compute; one more warp feeds them
+constexpr int kAdBlock = kAdThreads + 32;
 constexpr int kAdMaxRank = 128;
 constexpr int kAdMaxTokens = 8192;
 constexpr int kAdMaxSlots = 4096;
@@ -29,6 +37,12 @@ constexpr int kAdMaxD = 65536;
 constexpr int kAdInKernel = 256;    // up to this many tokens every block groups the ids itself
 constexpr int kAdGroups = 8;        // n8 rank groups of one pass over x: 64 ranks
 constexpr int kRedLd = 8 * kAdGroups + 8;
+constexpr uint64_t kAdSpin = 2000000000ull;  // about a second
+// Pieces of x and base, and of weights, on their way: what fits two blocks on an SM at 64 ranks.
+template <int XP, int VP>
+__host__ __device__ constexpr int ad_depth() { return XP == 1 && VP == 2 ? 4 : 3; }
+template <int TM, int XP, int VP>
+__host__ __device__ constexpr int ad_w_depth() { return TM == 64 && XP == 1 && VP == 2 ? 4 : 2; }
 
 struct AdMeta {
   int rank;     // 0: slot not loaded
@@ -52,18 +66,22 @@ struct AdArgs {
 
 __host__ __device__ constexpr int round16(int r) { return (r + 15) & ~15; }
 
+// Shared memory: barriers; the rings of x, then base, and the warps' sums [KG][TM][kRedLd] between them
+// in one place; the block's partial v; s v as VP bf16 parts; the weights' rings, a stage r16 x 64 bytes.
 struct AdSmem {
-  int red, part, v, v_part, total, v_ld;  // v: VP parts of v_part bytes
+  int ring, part, v, v_part, w, total, v_ld;
 };
-template <int TM, int VP>
+template <int TM, int XP, int VP>
 __host__ __device__ AdSmem ad_smem(int r16) {
+  constexpr int ring = ad_depth<XP, VP>() * kAdThreads * 16 * (XP == 1 && VP == 2 ? 2 : 4), red = kAdWarps * 16 * kRedLd * 4;
   AdSmem s;
   s.v_ld = r16 + 8;
-  s.red = 0;
-  s.part = s.red + kAdWarps * TM * kRedLd * 4;
+  s.ring = 512;
+  s.part = s.ring + (ring > red ? ring : red);
   s.v = s.part + TM * r16 * 4;
   s.v_part = TM * s.v_ld * 2;
-  s.total = s.v + VP * s.v_part;
+  s.w = (s.v + VP * s.v_part + 127) / 128 * 128;
+  s.total = s.w + kAdWarps / (TM / 16) * ad_w_depth<TM, XP, VP>() * r16 * 64;
   return s;
 }
 
@@ -104,11 +122,11 @@ __device__ __forceinline__ int ad_id(const AdArgs &a, int t, bool report) {
 // Returns the tile's token count (0: no such tile) and its adapter.
 template <int TM>
 __device__ int ad_find_tile(const AdArgs &a, int want, bool report, int *rows, int &adapter) {
-  __shared__ int s_id[kAdInKernel], s_warp[kAdWarps], s_got[2];
+  __shared__ int s_id[kAdInKernel], s_warp[kAdWarps + 1], s_got[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int id = -1;
   if (tid < a.n) id = ad_id(a, tid, report);
-  s_id[tid] = id;
+  if (tid < kAdInKernel) s_id[tid] = id;
   if (tid < 2) s_got[tid] = 0;
   __syncthreads();
   int before = 0, size = 0;
@@ -149,40 +167,241 @@ __device__ int ad_find_tile(const AdArgs &a, int want, bool report, int *rows, i
   return s_got[0];
 }
 
-// Eight consecutive values of a row as XP parts of four operand words (bf16 pairs); XP = 1: bf16 x.
-template <int XP>
-__device__ __forceinline__ void load_x8(const void *x, int64_t i, bool ok, uint32_t (&w)[XP][4]) {
-  if constexpr (XP == 1) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok) v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(x) + i));
-    w[0][0] = v.x; w[0][1] = v.y; w[0][2] = v.z; w[0][3] = v.w;
-  } else {
-    float4 u = make_float4(0, 0, 0, 0), v = u;
-    if (ok) {
-      const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-      u = __ldg(p);
-      v = __ldg(p + 1);
+// 16 bytes to this thread's slot; zeros where there is no source
+__device__ __forceinline__ void ad_copy(uint32_t dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ad_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int DEPTH>
+__device__ __forceinline__ void ad_wait() {  // all but the last DEPTH - 1 groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+}
+__device__ __forceinline__ void ad_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAdThreads) : "memory"); }
+__device__ __forceinline__ void ad_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// What both products of a tile share: a thread's place, its rows, its slots of the rings.
+struct AdLane {
+  int q, lane, row[2];  // row numbers of this lane's operand rows (16 mg + g and 16 mg + g + 8), or -1
+  uint32_t slot;        // this thread's first slot; the others lie kAdThreads * 16 bytes apart
+};
+constexpr uint32_t kSlots = kAdThreads * 16;
+
+// cp.async of a piece's 2 rows x 32 * B bytes a quad of lanes, B bytes a value, into `stage`; one group.
+template <int B>
+__device__ __forceinline__ void ad_piece(const AdLane &l, const char *const (&row)[2], int piece, int limit, int width, int stage) {
+  const int k = 32 * piece + 8 * l.q;
+  if (piece < limit) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool ok = l.row[h] >= 0 && k < width;
+      const char *src = ok ? row[h] + k * B : row[h];
+#pragma unroll
+      for (int c = 0; c < B / 2; ++c) ad_copy(l.slot + (stage * B + h * (B / 2) + c) * kSlots, src + (ok ? 16 * c : 0), ok);
     }
-    const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  }
+  ad_commit();
+}
+
+// The operand words of a piece of x: XP parts of rows g (0) and g + 8 (1), four words of two values.
+template <int XP>
+__device__ __forceinline__ void ad_operands(uint32_t src, uint32_t (&p)[XP][2][4]) {
+  if constexpr (XP == 1) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t parts[XP];
-      split_bf16x2<XP>(f[2 * k], f[2 * k + 1], parts);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 u = lds_u128(src + h * kSlots);
+      p[0][h][0] = u.x, p[0][h][1] = u.y, p[0][h][2] = u.z, p[0][h][3] = u.w;
+    }
+  } else {
 #pragma unroll
-      for (int i2 = 0; i2 < XP; ++i2) w[i2][k] = parts[i2];
+    for (int h = 0; h < 2; ++h) {
+      float2 f[4];
+      float most = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 u = lds_u128(src + (2 * h + c) * kSlots);
+        f[2 * c] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[2 * c + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        most = fmaxf(most, fmaxf(fmaxf(fabsf(f[2 * c].x), fabsf(f[2 * c].y)), fmaxf(fabsf(f[2 * c + 1].x), fabsf(f[2 * c + 1].y))));
+      }
+      const bool inf = most == __int_as_float(0x7F800000);
+#pragma unroll
+      for (int i = 0; i < XP; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[i][h][k] = i + 1 < XP ? cut_bf16x2(f[k], inf) : round_bf16x2(f[k]);
     }
   }
 }
 
+// A ring of weights: stages of `bytes`, filled in order; one for the warps of a kg.
+template <int DEPTH>
+struct AdRing {
+  uint64_t *full, *empty;
+  unsigned char *base;
+  int bytes, stage = 0, phase = 0;
+  __device__ AdRing(unsigned char *smem, const AdSmem &S, int r16, int kg, int kgs)
+      : full(reinterpret_cast<uint64_t *>(smem) + kg * DEPTH), empty(full + kgs * DEPTH), base(smem + S.w + kg * DEPTH * r16 * 64),
+        bytes(r16 * 64) {}
+  __device__ __forceinline__ void next() {
+    if (++stage == DEPTH) stage = 0, phase ^= 1;
+  }
+  // feeding lane: a piece of n bytes, when the stage is free
+  __device__ __forceinline__ bool put(const void *src, int n) {
+    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, kAdSpin)) return false;
+    mbar_arrive_expect_tx(&full[stage], n);
+    bulk_g2s(base + stage * bytes, src, n, &full[stage]);
+    next();
+    return true;
+  }
+  // A warp whose wait ran out sets the error word and does not wait again: what it then multiplies is
+  // in bounds, and every barrier is still reached.
+  __device__ __forceinline__ uint32_t take(uint64_t &limit, uint32_t *err) const {
+    if (!mbar_wait_bounded(&full[stage], phase, limit)) {
+      limit = 0;
+      flag_error(err, kErrTimeout);
+    }
+    return smem_u32(base + stage * bytes);
+  }
+  __device__ __forceinline__ void give() {  // this warp is done with the stage
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[stage]);
+    next();
+  }
+};
+
+// acc += A_i x over pieces kb, kb + KG, .. of x, for nj (2, 4, 6 or 8) groups of 8 ranks
+template <int KG, int XP, int VP, typename R>
+__device__ __forceinline__ void ad_shrink(const AdLane &l, const char *const (&row)[2], int kb, int kb1, int d_in, R &ring, int nj,
+                                          float (&acc)[kAdGroups][4], uint64_t &limit, uint32_t *err) {
+  constexpr int B = XP == 1 ? 2 : 4, D = ad_depth<XP, VP>();
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) ad_piece<B>(l, row, kb + i * KG, kb1, d_in, i);
+  int stage = 0;
+  for (; kb < kb1; kb += KG) {
+    ad_piece<B>(l, row, kb + (D - 1) * KG, kb1, d_in, stage == 0 ? D - 1 : stage - 1);
+    ad_wait<D>();
+    uint32_t p[XP][2][4];
+    ad_operands<XP>(l.slot + stage * B * kSlots, p);
+    const uint32_t w = ring.take(limit, err) + l.lane * 16;
+#pragma unroll
+    for (int j = 0; j < kAdGroups; j += 2)
+      if (j < nj) {
+        const uint4 u = lds_u128(w + 512 * j), v = lds_u128(w + 512 * j + 512);
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+          const uint32_t a0[4] = {p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1]};
+          const uint32_t a1[4] = {p[i][0][2], p[i][1][2], p[i][0][3], p[i][1][3]};
+          mma_bf16(acc[j], a0, u.x, u.y), mma_bf16(acc[j], a1, u.z, u.w);
+          mma_bf16(acc[j + 1], a0, v.x, v.y), mma_bf16(acc[j + 1], a1, v.z, v.w);
+        }
+      }
+    ring.give();
+    stage = stage == D - 1 ? 0 : stage + 1;
+  }
+  ad_wait_all();
+}
+
+// out = base + B_i v over columns 32 nb .., nb + KG, ..: a lane holds eight consecutive columns of its
+// rows (the packed B orders the MMA columns so), nk 16-rank steps; the first pieces of base are on their
+// way already.
+template <int KG, int XP, int VP, typename R>
+__device__ __forceinline__ void ad_expand(const AdLane &l, const char *const (&base)[2], char *const (&out)[2], int nb, int nb1,
+                                          int d_out, R &ring, int nk, uint32_t vaddr, int v_part, uint64_t &limit, uint32_t *err) {
+  constexpr int B = VP == 2 ? 2 : 4, D = ad_depth<XP, VP>();
+  int stage = 0;
+  for (; nb < nb1; nb += KG) {
+    ad_piece<B>(l, base, nb + (D - 1) * KG, nb1, d_out, stage == 0 ? D - 1 : stage - 1);
+    float acc[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+    const uint32_t w = ring.take(limit, err) + l.lane * 16;
+#pragma unroll 4
+    for (int k = 0; k < nk; ++k) {
+      const uint4 wa = lds_u128(w + 1024 * k), wb = lds_u128(w + 1024 * k + 512);
+#pragma unroll
+      for (int i = 0; i < VP; ++i) {
+        uint32_t v[4];
+        ldmatrix_x4(v, vaddr + i * v_part + 32 * k);
+        mma_bf16(acc[0], v, wa.x, wa.y);
+        mma_bf16(acc[1], v, wa.z, wa.w);
+        mma_bf16(acc[2], v, wb.x, wb.y);
+        mma_bf16(acc[3], v, wb.z, wb.w);
+      }
+    }
+    ring.give();
+    ad_wait<D>();
+    const int col = 32 * nb + 8 * l.q;
+    if (col < d_out)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (l.row[h] < 0) continue;
+        uint4 *o = reinterpret_cast<uint4 *>(out[h] + col * B);
+        const uint32_t src = l.slot + (stage * B + h * (B / 2)) * kSlots;
+        if (B == 2) {
+          const uint4 b = lds_u128(src);
+          const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(__uint_as_float(b4[j] << 16) + acc[j][2 * h],
+                                                           __uint_as_float(b4[j] & 0xFFFF0000u) + acc[j][2 * h + 1]);
+            r[j] = *reinterpret_cast<const uint32_t *>(&q);
+          }
+          o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4 b = lds_u128(src + c * kSlots);
+            o[c] = make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[2 * c][2 * h]),
+                              __float_as_uint(__uint_as_float(b.y) + acc[2 * c][2 * h + 1]),
+                              __float_as_uint(__uint_as_float(b.z) + acc[2 * c + 1][2 * h]),
+                              __float_as_uint(__uint_as_float(b.w) + acc[2 * c + 1][2 * h + 1]));
+          }
+        }
+      }
+    stage = stage == D - 1 ? 0 : stage + 1;
+  }
+  ad_wait_all();
+}
+
+// out = base: tokens without an adapter
+template <int KG, int B>
+__device__ __forceinline__ void ad_plain_rows(const AdLane &l, char *const (&out)[2], int nb, int nb1, int d_out,
+                                              const char *const (&base)[2]) {
+  ad_wait_all();
+  for (; nb < nb1; nb += KG) {
+    const int col = 32 * nb + 8 * l.q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (l.row[h] >= 0 && col < d_out)
+#pragma unroll
+        for (int c = 0; c < B / 2; ++c)
+          reinterpret_cast<uint4 *>(out[h] + col * B)[c] = reinterpret_cast<const uint4 *>(base[h] + col * B)[c];
+  }
+}
+
 template <int TM, int XP, int VP>
-__global__ void __launch_bounds__(kAdThreads) k_adapter(const __grid_constant__ AdArgs a) {
-  constexpr int MT = TM / 16;
+__global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__ AdArgs a) {
+  constexpr int MG = TM / 16, KG = kAdWarps / MG;
+  constexpr int XB = XP == 1 ? 2 : 4, IO = VP == 2 ? 2 : 4;  // bytes of a value of x; of base and out
+  constexpr int DW = ad_w_depth<TM, XP, VP>();
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int rows[TM];
-  const AdSmem S = ad_smem<TM, VP>(a.max_rank16);
-  float *red = reinterpret_cast<float *>(smem + S.red), *part = reinterpret_cast<float *>(smem + S.part);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const AdSmem S = ad_smem<TM, XP, VP>(a.max_rank16);
+  float *red = reinterpret_cast<float *>(smem + S.ring), *part = reinterpret_cast<float *>(smem + S.part);
+  const int tid = threadIdx.x, warp = tid >> 5, mg = warp % MG, kg = warp / MG;
   const int cl = cluster_nctarank(), cr = cluster_ctarank(), tile = blockIdx.x / cl;
+  if (tid == 0) {
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem);
+    for (int i = 0; i < KG * DW; ++i) {
+      mbar_init(&bars[i], 1);
+      mbar_init(&bars[KG * DW + i], MG);
+    }
+    fence_barrier_init();
+  }
+  griddep_wait();
+  griddep_launch();
 
   int adapter, cnt;
   if (a.n <= kAdInKernel) {
@@ -199,78 +418,88 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter(const __grid_constant__ 
   if (cnt == 0) return;  // the same for every block of the cluster
   AdMeta meta{0, 0.f};
   if (adapter < a.slots) meta = a.meta[adapter];
-  const int r16 = round16(meta.rank), ng = r16 / 8;
+  const int r16 = round16(meta.rank), ng = r16 / 8, nk = r16 / 16;
+  const int kb_all = (a.d_in + 31) / 32, kb0 = kb_all * cr / cl, kb1 = kb_all * (cr + 1) / cl;
+  const int nb_all = (a.d_out + 31) / 32, nb0 = nb_all * cr / cl, nb1 = nb_all * (cr + 1) / cl;
 
-  // row numbers of this lane's operand rows (16m + g and 16m + g + 8)
-  int row[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * m + 8 * h + g;
-      row[m][h] = i < cnt ? rows[i] : -1;
+  if (warp == kAdWarps) {
+    // ---- the feeding warp: lane kg fills the ring of the warps kg
+    const int lane = tid & 31;
+    const bool mine = lane < KG;
+    AdRing<DW> ring(smem, S, a.max_rank16, mine ? lane : 0, KG);
+    bool ok = mine;
+    const __nv_bfloat16 *ap = a.a + a.a_slot * adapter, *bp = a.b + a.b_slot * adapter;
+    for (int g0 = 0; g0 < ng; g0 += kAdGroups) {
+      const int nj = min(kAdGroups, ng - g0);
+      for (int kb = kb0 + lane; kb < kb1 && ok; kb += KG) ok = ring.put(ap + (static_cast<int64_t>(kb) * ng + g0) * 256, nj * 512);
     }
+    // the first pieces of the second product, then the block's part in the cluster's barriers
+    int nb = nb0 + lane, first = 0;
+    for (; nk && nb < nb1 && first < DW && ok; nb += KG, ++first) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024);
+    __syncwarp();
+    if (cl > 1) {
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+    }
+    for (; nk && nb < nb1 && ok; nb += KG) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024);
+    if (mine && !ok) flag_error(a.err, kErrTimeout);
+    __syncwarp();
+    if (cl > 1) cluster_wait();
+    return;
+  }
+
+  uint64_t limit = kAdSpin;
+  AdRing<DW> ring(smem, S, a.max_rank16, kg, KG);
+  AdLane l;
+  l.lane = tid & 31, l.q = tid & 3, l.slot = smem_u32(smem + S.ring) + tid * 16;
+  const int g = l.lane >> 2;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) l.row[h] = 16 * mg + g + 8 * h < cnt ? rows[16 * mg + g + 8 * h] : -1;
+  const int64_t at[2] = {l.row[0] < 0 ? 0 : l.row[0], l.row[1] < 0 ? 0 : l.row[1]};
 
   // ---- v = A_i x over this block's slice of d_in, 64 ranks a pass
-  const int kb_all = (a.d_in + 31) / 32, kb0 = kb_all * cr / cl, kb1 = kb_all * (cr + 1) / cl;
-  const __nv_bfloat16 *ap = a.a + a.a_slot * adapter;
-  for (int g0 = 0; g0 < ng; g0 += kAdGroups) {
-    const int nj = min(kAdGroups, ng - g0);
-    float acc[MT][kAdGroups][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
+  {
+    const char *const xr[2] = {static_cast<const char *>(a.x) + at[0] * a.x_ld * XB, static_cast<const char *>(a.x) + at[1] * a.x_ld * XB};
+    for (int g0 = 0; g0 < ng; g0 += kAdGroups) {
+      const int nj = min(kAdGroups, ng - g0);
+      float acc[kAdGroups][4];
 #pragma unroll
       for (int j = 0; j < kAdGroups; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.f;
-#pragma unroll 2
-    for (int kb = kb0 + warp; kb < kb1; kb += kAdWarps) {
-      const int k = 32 * kb + 8 * q;
-      uint32_t xw[MT][2][XP][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          load_x8<XP>(a.x, row[m][h] * a.x_ld + k, row[m][h] >= 0 && k < a.d_in, xw[m][h]);
-      const uint4 *w = reinterpret_cast<const uint4 *>(ap) + (static_cast<int64_t>(kb) * ng + g0) * 32 + lane;
-      uint4 bw[kAdGroups];
-#pragma unroll
-      for (int j = 0; j < kAdGroups; ++j)
-        if (j < nj) bw[j] = __ldg(w + 32 * j);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < XP; ++i) {
-          const uint32_t a0[4] = {xw[m][0][i][0], xw[m][1][i][0], xw[m][0][i][1], xw[m][1][i][1]};
-          const uint32_t a1[4] = {xw[m][0][i][2], xw[m][1][i][2], xw[m][0][i][3], xw[m][1][i][3]};
-#pragma unroll
-          for (int j = 0; j < kAdGroups; ++j)
-            if (j < nj) {
-              mma_bf16(acc[m][j], a0, bw[j].x, bw[j].y);
-              mma_bf16(acc[m][j], a1, bw[j].z, bw[j].w);
-            }
-        }
-    }
-    // the warps' sums meet in shared memory, added in warp order
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int k = 0; k < 4; ++k) acc[j][k] = 0.f;
+      ad_shrink<KG, XP, VP>(l, xr, kb0 + kg, kb1, a.d_in, ring, nj, acc, limit, a.err);
+      ad_sync();  // the rings are read: the warps' sums take their place
+      // added in the order of kg
 #pragma unroll
       for (int j = 0; j < kAdGroups; ++j)
         if (j < nj) {
-          float *p = red + (warp * TM + 16 * m + g) * kRedLd + 8 * j + 2 * q;
-          *reinterpret_cast<float2 *>(p) = make_float2(acc[m][j][0], acc[m][j][1]);
-          *reinterpret_cast<float2 *>(p + 8 * kRedLd) = make_float2(acc[m][j][2], acc[m][j][3]);
+          float *p = red + (kg * TM + 16 * mg + g) * kRedLd + 8 * j + 2 * l.q;
+          *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2 *>(p + 8 * kRedLd) = make_float2(acc[j][2], acc[j][3]);
         }
-    __syncthreads();
-    for (int i = tid; i < TM * 8 * nj; i += kAdThreads) {
-      const int t = i / (8 * nj), r = i - t * (8 * nj);
-      float s = 0.f;
+      ad_sync();
+      for (int i = tid; i < TM * 2 * nj; i += kAdThreads) {
+        const int t = i / (2 * nj), r = 4 * (i - t * (2 * nj));
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kAdWarps; ++w) s += red[(w * TM + t) * kRedLd + r];
-      part[t * r16 + 8 * g0 + r] = s;
+        for (int w = 0; w < KG; ++w) {
+          const float4 v = *reinterpret_cast<const float4 *>(red + (w * TM + t) * kRedLd + r);
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<float4 *>(part + t * r16 + 8 * g0 + r) = s;
+      }
+      ad_sync();
     }
-    __syncthreads();
   }
+
+  // ---- the first pieces of base do not wait for v
+  const char *const br[2] = {static_cast<const char *>(a.base) + at[0] * a.base_ld * IO,
+                             static_cast<const char *>(a.base) + at[1] * a.base_ld * IO};
+  char *const orow[2] = {static_cast<char *>(a.out) + at[0] * a.out_ld * IO, static_cast<char *>(a.out) + at[1] * a.out_ld * IO};
+#pragma unroll
+  for (int i = 0; i < ad_depth<XP, VP>() - 1; ++i) ad_piece<IO>(l, br, nb0 + kg + i * KG, nb1, a.d_out, i);
+
   // ---- the blocks' partial v, added in block order; s v in bf16 parts
   if (cl > 1) {
     cluster_arrive();
@@ -284,81 +513,35 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter(const __grid_constant__ 
     else
       s = part[i];
     if (r >= meta.rank) s = 0.f;  // padded ranks: 0 even where x holds infinities
-    uint32_t w[VP];
-    split_bf16x2<VP>(s * meta.scale, 0.f, w);
+    float2 f = make_float2(s * meta.scale, 0.f);
+    const bool inf = fabsf(f.x) == __int_as_float(0x7F800000);
 #pragma unroll
     for (int k = 0; k < VP; ++k)
-      reinterpret_cast<uint16_t *>(smem + S.v + k * S.v_part)[t * S.v_ld + r] = static_cast<uint16_t>(w[k]);
+      reinterpret_cast<uint16_t *>(smem + S.v + k * S.v_part)[t * S.v_ld + r] =
+          static_cast<uint16_t>(k + 1 < VP ? cut_bf16x2(f, inf) : round_bf16x2(f));
   }
-  __syncthreads();
+  ad_sync();
   if (cl > 1) cluster_arrive();  // done with the other blocks' shared memory; waited for at the end
 
-  // ---- out = base + B_i v over this block's slice of d_out, 32 columns a warp and step; a lane
-  // holds eight consecutive columns of its rows (the packed B orders the MMA columns so)
-  const int nb_all = (a.d_out + 31) / 32, nb0 = nb_all * cr / cl, nb1 = nb_all * (cr + 1) / cl;
-  const uint4 *bp = reinterpret_cast<const uint4 *>(a.b + a.b_slot * adapter);
-  const int nk = r16 / 16;
-  const uint32_t vaddr = smem_u32(smem + S.v) + ((lane & 15) * S.v_ld + (lane >> 4) * 8) * 2;
-  for (int nb = nb0 + warp; nb < nb1; nb += kAdWarps) {
-    const int col = 32 * nb + 8 * q;
-    float acc[MT][4][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.f;
-    for (int k = 0; k < nk; ++k) {
-      const uint4 *w = bp + ((static_cast<int64_t>(nb) * nk + k) * 32 + lane) * 2;
-      const uint4 w0 = __ldg(w), w1 = __ldg(w + 1);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-          uint32_t v[4];
-          ldmatrix_x4(v, vaddr + i * S.v_part + (16 * m * S.v_ld + 16 * k) * 2);
-          mma_bf16(acc[m][0], v, w0.x, w0.y);
-          mma_bf16(acc[m][1], v, w0.z, w0.w);
-          mma_bf16(acc[m][2], v, w1.x, w1.y);
-          mma_bf16(acc[m][3], v, w1.z, w1.w);
-        }
-      }
-    }
-    if (col >= a.d_out) continue;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = row[m][h];
-        if (t < 0) continue;
-        const int64_t ib = t * a.base_ld + col, io = t * a.out_ld + col;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = acc[m][j][2 * h];
-          v[2 * j + 1] = acc[m][j][2 * h + 1];
-        }
-        if (a.io_bf16) {
-          const uint4 b = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.base) + ib);
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(bw[j] << 16) + v[2 * j],
-                                                           __uint_as_float(bw[j] & 0xFFFF0000u) + v[2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t *>(&p);
-          }
-          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + io) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-          const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(a.base) + ib);
-          const float4 b0 = b[0], b1 = b[1];
-          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + io);
-          o[0] = make_float4(b0.x + v[0], b0.y + v[1], b0.z + v[2], b0.w + v[3]);
-          o[1] = make_float4(b1.x + v[4], b1.y + v[5], b1.z + v[6], b1.w + v[7]);
-        }
-      }
-  }
+  const uint32_t vaddr = smem_u32(smem + S.v) + ((16 * mg + (l.lane & 15)) * S.v_ld + (l.lane >> 4) * 8) * 2;
+  if (nk)
+    ad_expand<KG, XP, VP>(l, br, orow, nb0 + kg, nb1, a.d_out, ring, nk, vaddr, S.v_part, limit, a.err);
+  else
+    ad_plain_rows<KG, IO>(l, orow, nb0 + kg, nb1, a.d_out, br);
+  __syncwarp();
   if (cl > 1) cluster_wait();
+}
+
+// Takes the next place of counter id (ids below 0: none): one atomic for all of a warp's lanes with the
+// same id (a few long prompts put every lane on one counter: 15 us for 8,192 tokens without this).
+__device__ __forceinline__ int ad_take(int *counters, int id) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  const int leader = __ffs(same) - 1;
+  int at = 0;
+  if (lane == leader && id >= 0) at = atomicAdd(&counters[id], __popc(same));
+  at = __shfl_sync(0xffffffffu, at, leader);
+  return at + __popc(same & ((1u << lane) - 1u));
 }
 
 // Counting sort of the tokens by adapter and the list of tiles (more than kAdInKernel tokens); one
@@ -368,10 +551,18 @@ __global__ void __launch_bounds__(1024) k_adapter_group(AdArgs a, int4 *tiles, i
   extern __shared__ int s_cnt[];  // [slots + 1] counts, then cursors
   __shared__ int s_rows[32], s_tiles[32], s_base[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = a.slots + 1;
+  constexpr int kEach = kAdMaxTokens / 1024;
   for (int i = tid; i < groups; i += 1024) s_cnt[i] = 0;
   if (tid < 2) s_base[tid] = 0;
+  griddep_wait();
+  griddep_launch();
+  int id[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) id[k] = tid + 1024 * k < a.n ? ad_id(a, tid + 1024 * k, true) : -1;
   __syncthreads();
-  for (int t = tid; t < a.n; t += 1024) atomicAdd(&s_cnt[ad_id(a, t, true)], 1);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (1024 * k < a.n) ad_take(s_cnt, id[k]);
   __syncthreads();
   for (int i0 = 0; i0 < groups; i0 += 1024) {
     const int i = i0 + tid, c = i < groups ? s_cnt[i] : 0;
@@ -393,21 +584,26 @@ __global__ void __launch_bounds__(1024) k_adapter_group(AdArgs a, int4 *tiles, i
     __syncthreads();
   }
   if (tid == 0) *n_tiles = s_base[1];
-  for (int t = tid; t < a.n; t += 1024) order[atomicAdd(&s_cnt[ad_id(a, t, false)], 1)] = t;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (1024 * k < a.n) {
+      const int at = ad_take(s_cnt, id[k]);
+      if (id[k] >= 0) order[at] = tid + 1024 * k;
+    }
 }
 
 // A (rank x d_in) and B (d_out x rank) into the kernels' operand order, padded with zeros to 16
 // ranks and 32 columns.
 //   A: [k / 32][rank / 8][lane][8]: lane 4g + q holds A[8j + g][32 kb + 8q + e]
-//   B: [col / 32][rank / 16][lane][j][2][2]: MMA j, lane 4g + q, register h, element e holds column
-//      32 nb + 8 (g / 2) + 2j + g % 2 of rank 16 k + 8h + 2q + e
+//   B: [col / 32][rank / 16][j / 2][lane][j % 2][2][2]: MMA j, lane 4g + q, register h, element e holds
+//      column 32 nb + 8 (g / 2) + 2j + g % 2 of rank 16 k + 8h + 2q + e
 __global__ void __launch_bounds__(256) k_adapter_pack(const __nv_bfloat16 *src, __nv_bfloat16 *dst, int is_b, int rank, int d) {
   const int r16 = round16(rank), d32 = (d + 31) / 32 * 32;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(r16) * d32) return;
   int r, c;
   if (is_b) {
-    const int e = i & 1, h = (i >> 1) & 1, j = (i >> 2) & 3, lane = (i >> 4) & 31;
+    const int e = i & 1, h = (i >> 1) & 1, lane = (i >> 3) & 31, j = ((i >> 2) & 1) + 2 * ((i >> 8) & 1);
     const int64_t blk = i >> 9;
     const int nk = r16 / 16, k = blk % nk, nb = blk / nk, g = lane >> 2, q = lane & 3;
     r = 16 * k + 8 * h + 2 * q + e;
@@ -474,46 +670,51 @@ moe_status ad_cuda(moe_adapters *h, cudaError_t e, const char *what) {
 
 moe_status ad_pending(moe_adapters *h) {
   const uint32_t e = __atomic_exchange_n(h->err_host, 0u, __ATOMIC_ACQ_REL);
+  if (e & kErrTimeout) return ad_fail(h, MOE_ERR_TIMEOUT, "a device-side bounded wait ran out");
   return e ? ad_fail(h, MOE_ERR_DEVICE_FAULT, "an adapter id of an earlier call was out of range or not loaded") : MOE_OK;
 }
 
-int tile_rows(int n) { return n > 1024 ? 32 : 16; }
+int tile_rows(int n) { return n > 2048 ? 64 : n > 512 ? 32 : 16; }
 int64_t most_tiles(int n, int tm, int slots) { return n / tm + (n < slots + 1 ? n : slots + 1); }
 
-template <int TM, int XP, int VP>
-cudaError_t launch_adapter(const AdArgs &a, int clusters, int cl, cudaStream_t st) {
+// Launch in clusters of cl blocks, with programmatic stream serialization (the kernels wait for the one
+// before them themselves).
+struct AdConfig {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(clusters * cl);
-  cfg.blockDim = dim3(kAdThreads);
-  cfg.dynamicSmemBytes = ad_smem<TM, VP>(a.max_rank16).total;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cl;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_adapter<TM, XP, VP>, a);
-}
+  cudaLaunchAttribute at[2];
+  AdConfig(int grid, int threads, int smem, int cl, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cl;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cl > 1 ? 2 : 1;
+  }
+};
 
-template <int TM>
-cudaError_t launch_adapter_types(const AdArgs &a, int clusters, int cl, cudaStream_t st) {
-  if (a.io_bf16) return a.x_bf16 ? launch_adapter<TM, 1, 2>(a, clusters, cl, st) : launch_adapter<TM, 2, 2>(a, clusters, cl, st);
-  return a.x_bf16 ? launch_adapter<TM, 1, 3>(a, clusters, cl, st) : launch_adapter<TM, 3, 3>(a, clusters, cl, st);
+// f(TM, XP, VP) as constants, for every kernel
+template <int TM, typename F>
+cudaError_t each_type(F f) {
+  constexpr std::integral_constant<int, TM> tm{};
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 3> three{};
+  cudaError_t e = f(tm, one, two);
+  if (e == cudaSuccess) e = f(tm, two, two);
+  if (e == cudaSuccess) e = f(tm, one, three);
+  return e == cudaSuccess ? f(tm, three, three) : e;
 }
-
-template <int TM, int XP, int VP>
-cudaError_t configure_adapter() {
-  return cudaFuncSetAttribute(k_adapter<TM, XP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ad_smem<TM, VP>(kAdMaxRank).total);
-}
-template <int TM>
-cudaError_t configure_adapters() {
-  cudaError_t e = configure_adapter<TM, 1, 2>();
-  if (e == cudaSuccess) e = configure_adapter<TM, 2, 2>();
-  if (e == cudaSuccess) e = configure_adapter<TM, 1, 3>();
-  return e == cudaSuccess ? configure_adapter<TM, 3, 3>() : e;
+template <typename F>
+cudaError_t each_kernel(F f) {
+  cudaError_t e = each_type<16>(f);
+  if (e == cudaSuccess) e = each_type<32>(f);
+  return e == cudaSuccess ? each_type<64>(f) : e;
 }
 
 bool host_ptr(const void *p) {
@@ -585,8 +786,12 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
       e = cudaHostGetDevicePointer(reinterpret_cast<void **>(&h->err_dev), h->err_host, 0);
     }
     if (e == cudaSuccess) e = current_sm_count(&h->nsm);
-    if (e == cudaSuccess) e = configure_adapters<16>();
-    if (e == cudaSuccess) e = configure_adapters<32>();
+    if (e == cudaSuccess)
+      e = each_kernel([](auto tm, auto xp, auto vp) {
+        constexpr int TM = decltype(tm)::value, XP = decltype(xp)::value, VP = decltype(vp)::value;
+        return cudaFuncSetAttribute(k_adapter<TM, XP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    ad_smem<TM, XP, VP>(kAdMaxRank).total);
+      });
     if (e != cudaSuccess) s = ad_cuda(h, e, "adapters");
   }
   if (s != MOE_OK) {
@@ -680,13 +885,18 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   const int64_t tiles = most_tiles(n_tokens, tm, g.max_adapters);
   cudaError_t e = cudaSuccess;
   if (n_tokens > kAdInKernel) {
-    k_adapter_group<<<1, 1024, (g.max_adapters + 1) * 4, st>>>(a, h->tiles, h->order, h->n_tiles, tm);
-    e = cudaGetLastError();
+    const AdConfig c(1, 1024, (g.max_adapters + 1) * 4, 1, st);
+    e = cudaLaunchKernelEx(&c.cfg, k_adapter_group, a, h->tiles, h->order, h->n_tiles, tm);
   }
   int cl = 8;
   while (cl > 1 && tiles * cl > 2 * h->nsm) cl >>= 1;
   if (e == cudaSuccess)
-    e = tm == 16 ? launch_adapter_types<16>(a, tiles, cl, st) : launch_adapter_types<32>(a, tiles, cl, st);
+    e = each_kernel([&](auto tmc, auto xp, auto vp) {
+      constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value;
+      if (TM != tm || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;
+      const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, ad_smem<TM, XP, VP>(a.max_rank16).total, cl, st);
+      return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP>, a);
+    });
   return e == cudaSuccess ? MOE_OK : ad_cuda(h, e, "adapter launch");
 }
 

@@ -48,21 +48,21 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
-// Two floats as N bf16 pairs (the first float in the low half) that add up to them: to 2^-16 of a
-// value for N = 2, exactly (but for subnormal parts) for N = 3.  All parts but the last are cut, not
-// rounded, so that a large finite value never becomes an infinity.  An infinity has one part.
-template <int N>
-__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t (&out)[N]) {
-  const bool xi = (__float_as_uint(x) & 0x7FFFFFFFu) == 0x7F800000u, yi = (__float_as_uint(y) & 0x7FFFFFFFu) == 0x7F800000u;
-#pragma unroll
-  for (int i = 0; i + 1 < N; ++i) {
-    const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
-    out[i] = __byte_perm(xb, yb, 0x7632);
-    x = xi ? 0.f : x - __uint_as_float(xb & 0xFFFF0000u);
-    y = yi ? 0.f : y - __uint_as_float(yb & 0xFFFF0000u);
-  }
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x, y);
-  out[N - 1] = *reinterpret_cast<const uint32_t *>(&l);
+// A float as the sum of bf16 parts, two floats at a time (a pair, the first in the low half): cut_bf16x2
+// takes the upper halves of the floats and leaves the rest in f, round_bf16x2 rounds what is left.  One
+// cut and one rounding keep a value to 2^-16 of its magnitude, two cuts and one rounding exactly (but
+// for subnormal parts).  A part that is cut, not rounded, never becomes an infinity; an infinity (inf:
+// one may be among the values) has no rest.
+__device__ __forceinline__ uint32_t cut_bf16x2(float2 &f, bool inf) {
+  const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y), r = __byte_perm(x, y, 0x7632);
+  const float hx = __uint_as_float(x & 0xFFFF0000u), hy = __uint_as_float(y & 0xFFFF0000u);
+  f.x = inf && (x & 0x7FFFFFFFu) == 0x7F800000u ? 0.f : f.x - hx;
+  f.y = inf && (y & 0x7FFFFFFFu) == 0x7F800000u ? 0.f : f.y - hy;
+  return r;
+}
+__device__ __forceinline__ uint32_t round_bf16x2(const float2 &f) {
+  const __nv_bfloat162 l = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t *>(&l);
 }
 
 }  // namespace moe
