@@ -38,11 +38,12 @@ constexpr int kAdInKernel = 256;    // up to this many tokens every block groups
 constexpr int kAdGroups = 8;        // n8 rank groups of one pass over x: 64 ranks
 constexpr int kRedLd = 8 * kAdGroups + 8;
 constexpr uint64_t kAdSpin = 2000000000ull;  // about a second
-// Pieces of x and base, and of weights, on their way: what fits two blocks on an SM at 64 ranks.
-template <int XP, int VP>
-__host__ __device__ constexpr int ad_depth() { return XP == 1 && VP == 2 ? 4 : 3; }
-template <int TM, int XP, int VP>
-__host__ __device__ constexpr int ad_w_depth() { return TM == 64 && XP == 1 && VP == 2 ? 4 : 2; }
+// Pieces of x and base, and of weights, on their way: what fits two blocks on an SM at 32 ranks (RC = 0)
+// and at 64 (RC = 1).  In bytes they are what bounds long prompts: 64 KB an SM gave 3 TB/s.
+template <int XP, int VP, int RC>
+__host__ __device__ constexpr int ad_depth() { return XP == 1 && VP == 2 ? 4 : RC == 0 ? 4 : 3; }
+template <int TM, int XP, int VP, int RC>
+__host__ __device__ constexpr int ad_w_depth() { return TM != 64 ? 2 : RC == 0 || (XP == 1 && VP == 2) ? 4 : 2; }
 
 struct AdMeta {
   int rank;     // 0: slot not loaded
@@ -71,9 +72,9 @@ __host__ __device__ constexpr int round16(int r) { return (r + 15) & ~15; }
 struct AdSmem {
   int ring, part, v, v_part, w, total, v_ld;
 };
-template <int TM, int XP, int VP>
+template <int TM, int XP, int VP, int RC>
 __host__ __device__ AdSmem ad_smem(int r16) {
-  constexpr int ring = ad_depth<XP, VP>() * kAdThreads * 16 * (XP == 1 && VP == 2 ? 2 : 4), red = kAdWarps * 16 * kRedLd * 4;
+  constexpr int ring = ad_depth<XP, VP, RC>() * kAdThreads * 16 * (XP == 1 && VP == 2 ? 2 : 4), red = kAdWarps * 16 * kRedLd * 4;
   AdSmem s;
   s.v_ld = r16 + 8;
   s.ring = 512;
@@ -81,7 +82,7 @@ __host__ __device__ AdSmem ad_smem(int r16) {
   s.v = s.part + TM * r16 * 4;
   s.v_part = TM * s.v_ld * 2;
   s.w = (s.v + VP * s.v_part + 127) / 128 * 128;
-  s.total = s.w + kAdWarps / (TM / 16) * ad_w_depth<TM, XP, VP>() * r16 * 64;
+  s.total = s.w + kAdWarps / (TM / 16) * ad_w_depth<TM, XP, VP, RC>() * r16 * 64;
   return s;
 }
 
@@ -186,17 +187,20 @@ struct AdLane {
 };
 constexpr uint32_t kSlots = kAdThreads * 16;
 
-// cp.async of a piece's 2 rows x 32 * B bytes a quad of lanes, B bytes a value, into `stage`; one group.
+// cp.async of a piece's 2 rows x 32 values of B bytes a quad of lanes into `stage`; one group.  A lane
+// takes 16 bytes at a time, so that a quad's requests are whole sectors (its values of fp32 are two runs
+// of four, 4q and 16 + 4q, of bf16 one of eight, 8q: half sectors were fetched twice).
 template <int B>
 __device__ __forceinline__ void ad_piece(const AdLane &l, const char *const (&row)[2], int piece, int limit, int width, int stage) {
-  const int k = 32 * piece + 8 * l.q;
   if (piece < limit) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool ok = l.row[h] >= 0 && k < width;
-      const char *src = ok ? row[h] + k * B : row[h];
+    for (int c = 0; c < B / 2; ++c) {
+      const int k = 32 * piece + (B == 2 ? 8 * l.q : 16 * c + 4 * l.q);
 #pragma unroll
-      for (int c = 0; c < B / 2; ++c) ad_copy(l.slot + (stage * B + h * (B / 2) + c) * kSlots, src + (ok ? 16 * c : 0), ok);
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = l.row[h] >= 0 && k < width;
+        ad_copy(l.slot + (stage * B + h * (B / 2) + c) * kSlots, ok ? row[h] + k * B : row[h], ok);
+      }
     }
   }
   ad_commit();
@@ -269,10 +273,10 @@ struct AdRing {
 };
 
 // acc += A_i x over pieces kb, kb + KG, .. of x, for nj (2, 4, 6 or 8) groups of 8 ranks
-template <int KG, int XP, int VP, typename R>
+template <int KG, int XP, int VP, int RC, typename R>
 __device__ __forceinline__ void ad_shrink(const AdLane &l, const char *const (&row)[2], int kb, int kb1, int d_in, R &ring, int nj,
                                           float (&acc)[kAdGroups][4], uint64_t &limit, uint32_t *err) {
-  constexpr int B = XP == 1 ? 2 : 4, D = ad_depth<XP, VP>();
+  constexpr int B = XP == 1 ? 2 : 4, D = ad_depth<XP, VP, RC>();
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) ad_piece<B>(l, row, kb + i * KG, kb1, d_in, i);
   int stage = 0;
@@ -281,11 +285,18 @@ __device__ __forceinline__ void ad_shrink(const AdLane &l, const char *const (&r
     ad_wait<D>();
     uint32_t p[XP][2][4];
     ad_operands<XP>(l.slot + stage * B * kSlots, p);
-    const uint32_t w = ring.take(limit, err) + l.lane * 16;
+    const uint32_t w = ring.take(limit, err) + (XP == 1 ? l.lane * 16 : (l.lane & ~3) * 16 + l.q * 8);
 #pragma unroll
     for (int j = 0; j < kAdGroups; j += 2)
       if (j < nj) {
-        const uint4 u = lds_u128(w + 512 * j), v = lds_u128(w + 512 * j + 512);
+        uint4 u, v;
+        if (XP == 1) {
+          u = lds_u128(w + 512 * j), v = lds_u128(w + 512 * j + 512);
+        } else {  // the weights of fp32's order of k: half of two other lanes' words each
+          const uint2 a = lds_u64(w + 512 * j), b = lds_u64(w + 512 * j + 32);
+          const uint2 c = lds_u64(w + 512 * j + 512), d = lds_u64(w + 512 * j + 544);
+          u = make_uint4(a.x, a.y, b.x, b.y), v = make_uint4(c.x, c.y, d.x, d.y);
+        }
 #pragma unroll
         for (int i = 0; i < XP; ++i) {
           const uint32_t a0[4] = {p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1]};
@@ -300,14 +311,16 @@ __device__ __forceinline__ void ad_shrink(const AdLane &l, const char *const (&r
   ad_wait_all();
 }
 
-// out = base + B_i v over columns 32 nb .., nb + KG, ..: a lane holds eight consecutive columns of its
-// rows (the packed B orders the MMA columns so), nk 16-rank steps; the first pieces of base are on their
-// way already.
-template <int KG, int XP, int VP, typename R>
+// out = base + B_i v over columns 32 nb .., nb + KG, ..: a lane holds eight columns of its rows, 8q ..
+// for bf16 as the packed B orders the MMA columns, 4q .. and 16 + 4q .. for fp32 by taking other lanes'
+// words; nk 16-rank steps; the first pieces of base are on their way already.
+template <int KG, int XP, int VP, int RC, typename R>
 __device__ __forceinline__ void ad_expand(const AdLane &l, const char *const (&base)[2], char *const (&out)[2], int nb, int nb1,
                                           int d_out, R &ring, int nk, uint32_t vaddr, int v_part, uint64_t &limit, uint32_t *err) {
-  constexpr int B = VP == 2 ? 2 : 4, D = ad_depth<XP, VP>();
+  constexpr int B = VP == 2 ? 2 : 4, D = ad_depth<XP, VP, RC>();
   int stage = 0;
+  const int g = l.lane >> 2;
+  const uint32_t mine = B == 2 ? l.lane * 16 : ((g >> 1) & 1) * 512 + (4 * (2 * (g >> 2) + (g & 1)) + l.q) * 16;
   for (; nb < nb1; nb += KG) {
     ad_piece<B>(l, base, nb + (D - 1) * KG, nb1, d_out, stage == 0 ? D - 1 : stage - 1);
     float acc[4][4];
@@ -315,10 +328,10 @@ __device__ __forceinline__ void ad_expand(const AdLane &l, const char *const (&b
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    const uint32_t w = ring.take(limit, err) + l.lane * 16;
+    const uint32_t w = ring.take(limit, err) + mine;
 #pragma unroll 4
     for (int k = 0; k < nk; ++k) {
-      const uint4 wa = lds_u128(w + 1024 * k), wb = lds_u128(w + 1024 * k + 512);
+      const uint4 wa = lds_u128(w + 1024 * k), wb = lds_u128(w + 1024 * k + (B == 2 ? 512 : 256));
 #pragma unroll
       for (int i = 0; i < VP; ++i) {
         uint32_t v[4];
@@ -331,35 +344,29 @@ __device__ __forceinline__ void ad_expand(const AdLane &l, const char *const (&b
     }
     ring.give();
     ad_wait<D>();
-    const int col = 32 * nb + 8 * l.q;
-    if (col < d_out)
+#pragma unroll
+    for (int c = 0; c < B / 2; ++c) {
+      const int col = 32 * nb + (B == 2 ? 8 * l.q : 16 * c + 4 * l.q);
+      if (col >= d_out) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (l.row[h] < 0) continue;
-        uint4 *o = reinterpret_cast<uint4 *>(out[h] + col * B);
-        const uint32_t src = l.slot + (stage * B + h * (B / 2)) * kSlots;
-        if (B == 2) {
-          const uint4 b = lds_u128(src);
-          const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
-          uint32_t r[4];
+        const uint4 b = lds_u128(l.slot + (stage * B + h * (B / 2) + c) * kSlots);
+        const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+        uint32_t r[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j) {
+          if (B == 2) {
             const __nv_bfloat162 q = __floats2bfloat162_rn(__uint_as_float(b4[j] << 16) + acc[j][2 * h],
                                                            __uint_as_float(b4[j] & 0xFFFF0000u) + acc[j][2 * h + 1]);
             r[j] = *reinterpret_cast<const uint32_t *>(&q);
-          }
-          o[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint4 b = lds_u128(src + c * kSlots);
-            o[c] = make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[2 * c][2 * h]),
-                              __float_as_uint(__uint_as_float(b.y) + acc[2 * c][2 * h + 1]),
-                              __float_as_uint(__uint_as_float(b.z) + acc[2 * c + 1][2 * h]),
-                              __float_as_uint(__uint_as_float(b.w) + acc[2 * c + 1][2 * h + 1]));
+          } else {
+            r[j] = __float_as_uint(__uint_as_float(b4[j]) + acc[2 * c + (j >> 1)][2 * h + (j & 1)]);
           }
         }
+        *reinterpret_cast<uint4 *>(out[h] + col * B) = make_uint4(r[0], r[1], r[2], r[3]);
       }
+    }
     stage = stage == D - 1 ? 0 : stage + 1;
   }
   ad_wait_all();
@@ -381,14 +388,14 @@ __device__ __forceinline__ void ad_plain_rows(const AdLane &l, char *const (&out
   }
 }
 
-template <int TM, int XP, int VP>
+template <int TM, int XP, int VP, int RC>
 __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__ AdArgs a) {
   constexpr int MG = TM / 16, KG = kAdWarps / MG;
   constexpr int XB = XP == 1 ? 2 : 4, IO = VP == 2 ? 2 : 4;  // bytes of a value of x; of base and out
-  constexpr int DW = ad_w_depth<TM, XP, VP>();
+  constexpr int DW = ad_w_depth<TM, XP, VP, RC>();
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int rows[TM];
-  const AdSmem S = ad_smem<TM, XP, VP>(a.max_rank16);
+  const AdSmem S = ad_smem<TM, XP, VP, RC>(a.max_rank16);
   float *red = reinterpret_cast<float *>(smem + S.ring), *part = reinterpret_cast<float *>(smem + S.part);
   const int tid = threadIdx.x, warp = tid >> 5, mg = warp % MG, kg = warp / MG;
   const int cl = cluster_nctarank(), cr = cluster_ctarank(), tile = blockIdx.x / cl;
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
       for (int j = 0; j < kAdGroups; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[j][k] = 0.f;
-      ad_shrink<KG, XP, VP>(l, xr, kb0 + kg, kb1, a.d_in, ring, nj, acc, limit, a.err);
+      ad_shrink<KG, XP, VP, RC>(l, xr, kb0 + kg, kb1, a.d_in, ring, nj, acc, limit, a.err);
       ad_sync();  // the rings are read: the warps' sums take their place
       // added in the order of kg
 #pragma unroll
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
                              static_cast<const char *>(a.base) + at[1] * a.base_ld * IO};
   char *const orow[2] = {static_cast<char *>(a.out) + at[0] * a.out_ld * IO, static_cast<char *>(a.out) + at[1] * a.out_ld * IO};
 #pragma unroll
-  for (int i = 0; i < ad_depth<XP, VP>() - 1; ++i) ad_piece<IO>(l, br, nb0 + kg + i * KG, nb1, a.d_out, i);
+  for (int i = 0; i < ad_depth<XP, VP, RC>() - 1; ++i) ad_piece<IO>(l, br, nb0 + kg + i * KG, nb1, a.d_out, i);
 
   // ---- the blocks' partial v, added in block order; s v in bf16 parts
   if (cl > 1) {
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
 
   const uint32_t vaddr = smem_u32(smem + S.v) + ((16 * mg + (l.lane & 15)) * S.v_ld + (l.lane >> 4) * 8) * 2;
   if (nk)
-    ad_expand<KG, XP, VP>(l, br, orow, nb0 + kg, nb1, a.d_out, ring, nk, vaddr, S.v_part, limit, a.err);
+    ad_expand<KG, XP, VP, RC>(l, br, orow, nb0 + kg, nb1, a.d_out, ring, nk, vaddr, S.v_part, limit, a.err);
   else
     ad_plain_rows<KG, IO>(l, orow, nb0 + kg, nb1, a.d_out, br);
   __syncwarp();
@@ -698,23 +705,27 @@ struct AdConfig {
   }
 };
 
-// f(TM, XP, VP) as constants, for every kernel
-template <int TM, typename F>
+// f(TM, XP, VP, RC) as constants, for every kernel
+template <int TM, int RC, typename F>
 cudaError_t each_type(F f) {
   constexpr std::integral_constant<int, TM> tm{};
+  constexpr std::integral_constant<int, RC> rc{};
   constexpr std::integral_constant<int, 1> one{};
   constexpr std::integral_constant<int, 2> two{};
   constexpr std::integral_constant<int, 3> three{};
-  cudaError_t e = f(tm, one, two);
-  if (e == cudaSuccess) e = f(tm, two, two);
-  if (e == cudaSuccess) e = f(tm, one, three);
-  return e == cudaSuccess ? f(tm, three, three) : e;
+  cudaError_t e = f(tm, one, two, rc);
+  if (e == cudaSuccess) e = f(tm, two, two, rc);
+  if (e == cudaSuccess) e = f(tm, one, three, rc);
+  return e == cudaSuccess ? f(tm, three, three, rc) : e;
 }
 template <typename F>
 cudaError_t each_kernel(F f) {
-  cudaError_t e = each_type<16>(f);
-  if (e == cudaSuccess) e = each_type<32>(f);
-  return e == cudaSuccess ? each_type<64>(f) : e;
+  cudaError_t e = each_type<16, 0>(f);
+  if (e == cudaSuccess) e = each_type<32, 0>(f);
+  if (e == cudaSuccess) e = each_type<64, 0>(f);
+  if (e == cudaSuccess) e = each_type<16, 1>(f);
+  if (e == cudaSuccess) e = each_type<32, 1>(f);
+  return e == cudaSuccess ? each_type<64, 1>(f) : e;
 }
 
 bool host_ptr(const void *p) {
@@ -787,10 +798,10 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
     }
     if (e == cudaSuccess) e = current_sm_count(&h->nsm);
     if (e == cudaSuccess)
-      e = each_kernel([](auto tm, auto xp, auto vp) {
-        constexpr int TM = decltype(tm)::value, XP = decltype(xp)::value, VP = decltype(vp)::value;
-        return cudaFuncSetAttribute(k_adapter<TM, XP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    ad_smem<TM, XP, VP>(kAdMaxRank).total);
+      e = each_kernel([](auto tm, auto xp, auto vp, auto rc) {
+        constexpr int TM = decltype(tm)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
+        return cudaFuncSetAttribute(k_adapter<TM, XP, VP, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    ad_smem<TM, XP, VP, RC>(RC ? kAdMaxRank : 32).total);
       });
     if (e != cudaSuccess) s = ad_cuda(h, e, "adapters");
   }
@@ -891,11 +902,11 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   int cl = 8;
   while (cl > 1 && tiles * cl > 2 * h->nsm) cl >>= 1;
   if (e == cudaSuccess)
-    e = each_kernel([&](auto tmc, auto xp, auto vp) {
-      constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value;
-      if (TM != tm || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;
-      const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, ad_smem<TM, XP, VP>(a.max_rank16).total, cl, st);
-      return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP>, a);
+    e = each_kernel([&](auto tmc, auto xp, auto vp, auto rc) {
+      constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
+      if (TM != tm || (RC == 0) != (h->r16 <= 32) || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;
+      const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, ad_smem<TM, XP, VP, RC>(a.max_rank16).total, cl, st);
+      return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP, RC>, a);
     });
   return e == cudaSuccess ? MOE_OK : ad_cuda(h, e, "adapter launch");
 }
