@@ -589,11 +589,15 @@ __global__ void __launch_bounds__(256) k_ffn_sum(SumArgs a) {
 // ------------------------------------------------------------------------------------------
 // few tokens: mma.sync m16n8k16 with the weights as the 16-row operand, straight from global
 // memory (a lane's 16-byte load is its operand of two MMAs: the order of k inside 32 is the same
-// on both sides, so it does not matter), the tokens as the 8-column operand.  The block's warps
-// take interleaved pieces of 32 k; their sums meet in shared memory and are added in warp order.
+// on both sides, so it does not matter), the tokens as the 8-column operand.  A cluster of CL blocks
+// has 16 rows; its blocks take runs of k, their warps interleaved pieces of 64 k (128 bytes of a row);
+// the sums meet in shared memory, then over the cluster, and are added in warp and block order.
+// Bound by the weights' bytes: what counts is loads on their way, so there are four or more blocks an
+// SM and eight weight loads a lane (8 tokens, d 2,048, f 8,192: one block an SM in the down product
+// gave 1.3 TB/s, with clusters of four).
 // ------------------------------------------------------------------------------------------
 constexpr int kSmThreads = 256, kSmWarps = 8;
-constexpr int kSmallMax = 32;  // tokens
+constexpr int kSmallMax = 8;  // tokens: the MMA's columns (16 in two column groups took 38 us, in k_ffn_gemm 35)
 
 struct SmallArgs {
   const __nv_bfloat16 *x, *wg, *wu, *wd;
@@ -605,101 +609,135 @@ struct SmallArgs {
   int n, d, f, add_bf16, y_bf16;
 };
 
-// acc[t] += rows r0 (lanes' g) and r1 (g + 8) of 16 weight rows times the tokens' rows x
-template <int NT>
-__device__ __forceinline__ void small_mma(const __nv_bfloat16 *r0, const __nv_bfloat16 *r1, bool ok0, bool ok1,
-                                          const __nv_bfloat16 *x, int64_t x_ld, int n, int k_all, float (&acc)[NT][4]) {
+// acc = rows r0 (lanes' g) and r1 (g + 8) of 16 weight rows times the tokens' rows x, summed over
+// the cluster; true in the lanes that hold the result (warp 0 of block 0).  `ready` is called before x
+// is read.
+template <typename F>
+__device__ __forceinline__ bool small_product(const __nv_bfloat16 *r0, const __nv_bfloat16 *r1, bool ok0, bool ok1,
+                                              const __nv_bfloat16 *x, int64_t x_ld, int n, int k_all, float (&acc)[4], F ready) {
+  __shared__ float red[kSmWarps - 1][4][32];
+  __shared__ float part[4][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  uint32_t cl, cr;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(cr));
+  const int pieces = (k_all + 63) / 64, p0 = static_cast<int>(pieces * cr / cl) + warp, p1 = static_cast<int>(pieces * (cr + 1) / cl);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int kb = warp; kb < (k_all + 31) / 32; kb += kSmWarps) {
-    const int k = 32 * kb + 8 * q;
-    const bool in = k < k_all;
-    const uint4 w0 = ok0 && in ? __ldg(reinterpret_cast<const uint4 *>(r0 + k)) : zero;
-    const uint4 w1 = ok1 && in ? __ldg(reinterpret_cast<const uint4 *>(r1 + k)) : zero;
-    const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
+  constexpr int AHEAD = 2;  // pieces of weights on their way
+  uint4 w[AHEAD][2][2];
+  auto fetch = [&](int p, uint4 (&to)[2][2]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int row = 8 * t + g;
-      const uint4 b = row < n && in ? __ldg(reinterpret_cast<const uint4 *>(x + row * x_ld + k)) : zero;
-      mma_bf16(acc[t], a0, b.x, b.y);
-      mma_bf16(acc[t], a1, b.z, b.w);
+    for (int s = 0; s < 2; ++s) {
+      const int k = 64 * p + 32 * s + 8 * q;
+      const bool in = p < p1 && k < k_all;
+      to[0][s] = ok0 && in ? __ldg(reinterpret_cast<const uint4 *>(r0 + k)) : zero;
+      to[1][s] = ok1 && in ? __ldg(reinterpret_cast<const uint4 *>(r1 + k)) : zero;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) fetch(p0 + i * kSmWarps, w[i]);
+  ready();
+  for (int p = p0; p < p1; p += AHEAD * kSmWarps) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int at = p + i * kSmWarps;
+      uint4 b[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int k = 64 * at + 32 * s + 8 * q;
+        b[s] = g < n && at < p1 && k < k_all ? *reinterpret_cast<const uint4 *>(x + g * x_ld + k) : zero;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t a0[4] = {w[i][0][s].x, w[i][1][s].x, w[i][0][s].y, w[i][1][s].y};
+        const uint32_t a1[4] = {w[i][0][s].z, w[i][1][s].z, w[i][0][s].w, w[i][1][s].w};
+        mma_bf16(acc, a0, b[s].x, b[s].y);
+        mma_bf16(acc, a1, b[s].z, b[s].w);
+      }
+      fetch(at + AHEAD * kSmWarps, w[i]);
+    }
+  }
+  if (warp)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp - 1][i][lane] = acc[i];
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int v = 0; v < kSmWarps - 1; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += red[v][i][lane];
+  }
+  if (cl == 1) return warp == 0;
+  if (warp == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[i][lane] = acc[i];
+  cluster_sync();
+  const bool mine = warp == 0 && cr == 0;
+  if (mine)
+    for (uint32_t c = 1; c < cl; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t at;
+        float v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&part[i][lane])), "r"(c));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        acc[i] += v;
+      }
+  cluster_sync();  // a block's sums are read before it leaves
+  return mine;
+}
+
+// Cluster: 8 rows of Wg (operand rows 0..7) and the same 8 of Wu (8..15): a lane gets g and u of the
+// same row and tokens.
+__global__ void __launch_bounds__(kSmThreads, 4) k_ffn_up(SmallArgs a, int cl) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, row = blockIdx.x / cl * 8 + g;
+  float acc[4] = {};
+  const bool ok = row < a.f;
+  griddep_wait();
+  griddep_launch();
+  const bool mine = small_product(a.wg + static_cast<int64_t>(row) * a.d, a.wu + static_cast<int64_t>(row) * a.d, ok, ok, a.x,
+                                      a.x_ld, a.n, a.d, acc, [] {});
+  if (!mine || !ok) return;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int tok = 2 * q + e;
+    if (tok >= a.n) continue;
+    const float gv = acc[e], uv = acc[2 + e];
+    const int64_t at = static_cast<int64_t>(tok) * a.f + row;
+    a.h[at] = __float2bfloat16_rn(gv * sigmoid_f(gv) * uv);
+    if (a.g) {
+      a.g[at] = gv;
+      a.u[at] = uv;
     }
   }
 }
 
-// Sum over the block's warps, in warp order, of warp 0's view: red [warps - 1][NT * 4][32].
-template <int NT>
-__device__ __forceinline__ bool small_reduce(float (&acc)[NT][4], float *red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp)
+// Cluster: 16 rows of Wd.  Launched while k_ffn_up ends (which began when everything before it had
+// completed), it has weights on their way before it waits for h.
+__global__ void __launch_bounds__(kSmThreads, 4) k_ffn_down(SmallArgs a, int cl) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, r0 = blockIdx.x / cl * 16 + g, r1 = r0 + 8;
+  float acc[4] = {};
+  const bool mine = small_product(a.wd + static_cast<int64_t>(r0) * a.f, a.wd + static_cast<int64_t>(r1) * a.f, r0 < a.d, r1 < a.d,
+                                      a.h, a.f, a.n, a.f, acc, [] {
+                                        griddep_wait();
+                                        griddep_launch();
+                                      });
+  if (!mine) return;
 #pragma unroll
-    for (int i = 0; i < NT * 4; ++i) red[((warp - 1) * NT * 4 + i) * 32 + lane] = acc[i >> 2][i & 3];
-  __syncthreads();
-  if (warp) return false;
-  for (int w = 0; w < kSmWarps - 1; ++w)
-#pragma unroll
-    for (int i = 0; i < NT * 4; ++i) acc[i >> 2][i & 3] += red[(w * NT * 4 + i) * 32 + lane];
-  return true;
-}
-
-// Block: 8 rows of Wg (operand rows 0..7) and the same 8 of Wu (8..15): a lane gets g and u of the
-// same row and tokens.
-template <int NT>
-__global__ void __launch_bounds__(kSmThreads) k_ffn_up(SmallArgs a) {
-  __shared__ float red[(kSmWarps - 1) * NT * 4 * 32];
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, row = blockIdx.x * 8 + g;
-  griddep_wait();
-  griddep_launch();
-  float acc[NT][4] = {};
-  const bool ok = row < a.f;
-  small_mma<NT>(a.wg + static_cast<int64_t>(row) * a.d, a.wu + static_cast<int64_t>(row) * a.d, ok, ok, a.x, a.x_ld, a.n,
-                a.d, acc);
-  if (!small_reduce<NT>(acc, red) || !ok) return;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int tok = 8 * t + 2 * q + e;
-      if (tok >= a.n) continue;
-      const float gv = acc[t][e], uv = acc[t][2 + e];
-      const int64_t at = static_cast<int64_t>(tok) * a.f + row;
-      a.h[at] = __float2bfloat16_rn(gv * sigmoid_f(gv) * uv);
-      if (a.g) {
-        a.g[at] = gv;
-        a.u[at] = uv;
-      }
+  for (int e = 0; e < 4; ++e) {
+    const int tok = 2 * q + (e & 1), row = e < 2 ? r0 : r1;
+    if (tok >= a.n || row >= a.d) continue;
+    float v = acc[e];
+    if (a.add) {
+      const int64_t at = tok * a.add_ld + row;
+      v += a.add_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[at]) : static_cast<const float *>(a.add)[at];
     }
-}
-
-// Block: 16 rows of Wd.
-template <int NT>
-__global__ void __launch_bounds__(kSmThreads) k_ffn_down(SmallArgs a) {
-  __shared__ float red[(kSmWarps - 1) * NT * 4 * 32];
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, r0 = blockIdx.x * 16 + g, r1 = r0 + 8;
-  griddep_wait();
-  griddep_launch();
-  float acc[NT][4] = {};
-  small_mma<NT>(a.wd + static_cast<int64_t>(r0) * a.f, a.wd + static_cast<int64_t>(r1) * a.f, r0 < a.d, r1 < a.d, a.h,
-                a.f, a.n, a.f, acc);
-  if (!small_reduce<NT>(acc, red)) return;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int tok = 8 * t + 2 * q + (e & 1), row = e < 2 ? r0 : r1;
-      if (tok >= a.n || row >= a.d) continue;
-      float v = acc[t][e];
-      if (a.add) {
-        const int64_t at = tok * a.add_ld + row;
-        v += a.add_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[at]) : static_cast<const float *>(a.add)[at];
-      }
-      const int64_t at = tok * a.y_ld + row;
-      if (a.y_bf16)
-        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
-      else
-        static_cast<float *>(a.y)[at] = v;
-    }
+    const int64_t at = tok * a.y_ld + row;
+    if (a.y_bf16)
+      static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
+    else
+      static_cast<float *>(a.y)[at] = v;
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -843,11 +881,19 @@ cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
   return f.cg == 1 ? cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 1>, a) : cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 2>, a);
 }
 
-template <int NT>
-cudaError_t launch_small(const SmallArgs &s, int up, int down, cudaStream_t st) {
-  const Config cu(up, kSmThreads, 0, 1, st), cd(down, kSmThreads, 0, 1, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cu.cfg, k_ffn_up<NT>, s);
-  return e == cudaSuccess ? cudaLaunchKernelEx(&cd.cfg, k_ffn_down<NT>, s) : e;
+// Blocks of a cluster over k: enough clusters x blocks for four an SM, each of eight pieces of 64 at
+// least (one for every warp).
+int small_cluster(int tiles, int k) {
+  int cl = 1;
+  while (cl < 8 && tiles * cl < 4 * 148 && (k + 63) / 64 >= 16 * cl) cl *= 2;
+  return cl;
+}
+
+cudaError_t launch_small(const SmallArgs &s, cudaStream_t st) {
+  const int up = (s.f + 7) / 8, down = (s.d + 15) / 16, cu = small_cluster(up, s.d), cd = small_cluster(down, s.f);
+  const Config u(up * cu, kSmThreads, 0, cu, st), d(down * cd, kSmThreads, 0, cd, st);
+  const cudaError_t e = cudaLaunchKernelEx(&u.cfg, k_ffn_up, s, cu);
+  return e == cudaSuccess ? cudaLaunchKernelEx(&d.cfg, k_ffn_down, s, cd) : e;
 }
 
 constexpr int kMaxDim = 65536;
@@ -923,8 +969,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     s.y = p->y, s.y_ld = p->y_stride, s.y_bf16 = p->y_dtype == MOE_BF16;
     s.h = h, s.g = static_cast<float *>(p->save_gate), s.u = static_cast<float *>(p->save_up);
     s.n = n, s.d = d, s.f = f;
-    const int gu = (f + 7) / 8, gd = (d + 15) / 16;
-    e = n <= 8 ? launch_small<1>(s, gu, gd, st) : n <= 16 ? launch_small<2>(s, gu, gd, st) : launch_small<4>(s, gu, gd, st);
+    e = launch_small(s, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   FfnDevice dev{};
