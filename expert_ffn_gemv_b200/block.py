@@ -144,16 +144,17 @@ class Adapters:
         """Puts an adapter into `slot`: a [rank, d_in], b [d_out, rank], bf16, contiguous, on the handle's
         device or in host memory; a = b = None empties the slot."""
         rank = 0
-        if a is not None or b is not None:
+        if (a is None) != (b is None):
+            _bad("a, b", "one is missing")
+        if a is not None:
             rank = a.shape[0] if a.dim() == 2 else -1
             for t, name, shape in ((a, "a", (rank, self.d_in)), (b, "b", (self.d_out, rank))):
                 if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous():
                     _bad(name, f"{t.dtype} {tuple(t.shape)}, expected contiguous bfloat16 {shape}")
                 if t.device.type != "cpu" and t.device != self.device:
                     _bad(name, f"on {t.device}, expected {self.device} or the host")
-        with torch.cuda.device(self.device):
-            self._check(_lib.moe_adapters_load(self.h, slot, P._ptr(a), P._ptr(b), rank, scale,
-                                               torch.cuda.current_stream().cuda_stream), "moe_adapters_load")
+        self._check(_lib.moe_adapters_load(self.h, slot, P._ptr(a), P._ptr(b), rank, scale,
+                                           torch.cuda.current_stream(self.device).cuda_stream), "moe_adapters_load")
 
     def apply(self, x, base, ids, out=None):
         """x [n, d_in]; base [n, d_out]; ids int32 [n]; returns out (base's type; may be base itself)."""

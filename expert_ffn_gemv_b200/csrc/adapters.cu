@@ -19,8 +19,10 @@
 // Precision: products of bf16 values with fp32 accumulators.  What is not bf16 by itself (fp32 x, and
 // v between the two products) enters as bf16 parts that add up to it: two where out is bf16 (2^-16 of
 // a value, far below the rounding of out), three where out is fp32 (exact).
+#include <mutex>
 #include <new>
 #include <string>
+#include <vector>
 
 #include "block.cuh"
 
@@ -604,9 +606,14 @@ __global__ void __launch_bounds__(1024) k_adapter_group(AdArgs a, int4 *tiles, i
 //   A: [k / 32][rank / 8][lane][8]: lane 4g + q holds A[8j + g][32 kb + 8q + e]
 //   B: [col / 32][rank / 16][j / 2][lane][j % 2][2][2]: MMA j, lane 4g + q, register h, element e holds
 //      column 32 nb + 8 (g / 2) + 2j + g % 2 of rank 16 k + 8h + 2q + e
-__global__ void __launch_bounds__(256) k_adapter_pack(const __nv_bfloat16 *src, __nv_bfloat16 *dst, int is_b, int rank, int d) {
-  const int r16 = round16(rank), d32 = (d + 31) / 32 * 32;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+// One launch packs both matrices (blocks from `blocks_a` on: B) and sets the slot's rank and scale.
+__global__ void __launch_bounds__(256) k_adapter_pack(const __nv_bfloat16 *a, const __nv_bfloat16 *b, __nv_bfloat16 *pa, __nv_bfloat16 *pb,
+                                                      AdMeta *meta, AdMeta m, int d_in, int d_out, int blocks_a) {
+  const int rank = m.rank, r16 = round16(rank), block = blockIdx.x;
+  if (block == 0 && threadIdx.x == 0) *meta = m;
+  const bool is_b = block >= blocks_a;
+  const int d = is_b ? d_out : d_in, d32 = (d + 31) / 32 * 32;
+  const int64_t i = static_cast<int64_t>(is_b ? block - blocks_a : block) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(r16) * d32) return;
   int r, c;
   if (is_b) {
@@ -623,10 +630,41 @@ __global__ void __launch_bounds__(256) k_adapter_pack(const __nv_bfloat16 *src, 
     c = 32 * kb + 8 * (lane & 3) + e;
   }
   const bool in = r < rank && c < d;
-  dst[i] = in ? (is_b ? src[static_cast<int64_t>(c) * rank + r] : src[static_cast<int64_t>(r) * d + c]) : __float2bfloat16_rn(0.f);
+  (is_b ? pb : pa)[i] = in ? (is_b ? b[static_cast<int64_t>(c) * rank + r] : a[static_cast<int64_t>(r) * d + c]) : __float2bfloat16_rn(0.f);
 }
 
-__global__ void k_adapter_meta(AdMeta *m, AdMeta v) { *m = v; }
+// Error words in host memory that every device can write: handed out from pages that stay with the
+// process, since pinning one for each handle takes longer than everything else in its creation.
+class ErrorWords {
+ public:
+  uint32_t *take() {
+    std::lock_guard<std::mutex> lock(mutex_);
+    if (free_.empty()) {
+      uint32_t *page = nullptr;
+      if (cudaHostAlloc(reinterpret_cast<void **>(&page), 4096, cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+      }
+      for (int i = 0; i < 4096 / 64; ++i) free_.push_back(page + 16 * i);
+    }
+    uint32_t *w = free_.back();
+    free_.pop_back();
+    *w = 0;
+    return w;
+  }
+  void give(uint32_t *w) {
+    std::lock_guard<std::mutex> lock(mutex_);
+    free_.push_back(w);
+  }
+
+ private:
+  std::mutex mutex_;
+  std::vector<uint32_t *> free_;
+};
+ErrorWords &error_words() {
+  static ErrorWords *words = new ErrorWords;  // outlives every handle
+  return *words;
+}
 
 struct Device {
   int prev = -1;
@@ -728,6 +766,20 @@ cudaError_t each_kernel(F f) {
   return e == cudaSuccess ? each_type<64, 1>(f) : e;
 }
 
+// The kernels' shared-memory limit, once per device, with it current.
+cudaError_t configure_kernels(int dev) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> done[kMaxDevices];
+  if (dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = each_kernel([](auto tm, auto xp, auto vp, auto rc) {
+    constexpr int TM = decltype(tm)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
+    return cudaFuncSetAttribute(k_adapter<TM, XP, VP, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ad_smem<TM, XP, VP, RC>(RC ? kAdMaxRank : 32).total);
+  });
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 bool host_ptr(const void *p) {
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
@@ -769,9 +821,8 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
     off = (off + bytes + 255) & ~uint64_t(255);
     return at;
   };
-  const uint64_t d_max = g.d_in > g.d_out ? g.d_in : g.d_out;
   const uint64_t oa = take(h->a_slot * 2 * g.max_adapters), ob = take(h->b_slot * 2 * g.max_adapters);
-  const uint64_t os = take(d_max * g.max_rank * 2), om = take(sizeof(AdMeta) * g.max_adapters);
+  const uint64_t os = take((static_cast<uint64_t>(g.d_in) + g.d_out) * g.max_rank * 2), om = take(sizeof(AdMeta) * g.max_adapters);
   const uint64_t ot = take(16 * (g.max_tokens / 16 + g.max_adapters + 2)), oo = take(4ull * g.max_tokens), on = take(4);
   cudaError_t e = cudaMalloc(&h->mem, off);
   moe_status s = MOE_OK;
@@ -790,19 +841,12 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
     h->n_tiles = reinterpret_cast<int *>(p + on);
     e = cudaMemset(h->meta, 0, sizeof(AdMeta) * g.max_adapters);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    if (e == cudaSuccess)
-      e = cudaHostAlloc(reinterpret_cast<void **>(&h->err_host), sizeof(uint32_t), cudaHostAllocMapped);
     if (e == cudaSuccess) {
-      *h->err_host = 0;
-      e = cudaHostGetDevicePointer(reinterpret_cast<void **>(&h->err_dev), h->err_host, 0);
+      h->err_host = error_words().take();
+      e = h->err_host ? cudaHostGetDevicePointer(reinterpret_cast<void **>(&h->err_dev), h->err_host, 0) : cudaErrorMemoryAllocation;
     }
     if (e == cudaSuccess) e = current_sm_count(&h->nsm);
-    if (e == cudaSuccess)
-      e = each_kernel([](auto tm, auto xp, auto vp, auto rc) {
-        constexpr int TM = decltype(tm)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
-        return cudaFuncSetAttribute(k_adapter<TM, XP, VP, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    ad_smem<TM, XP, VP, RC>(RC ? kAdMaxRank : 32).total);
-      });
+    if (e == cudaSuccess) e = configure_kernels(g.device);
     if (e != cudaSuccess) s = ad_cuda(h, e, "adapters");
   }
   if (s != MOE_OK) {
@@ -818,7 +862,7 @@ moe_status moe_adapters_destroy(moe_adapters *h) {
   Device dev(h->cfg.device);
   cudaDeviceSynchronize();
   if (h->mem) cudaFree(h->mem);
-  if (h->err_host) cudaFreeHost(h->err_host);
+  if (h->err_host) error_words().give(h->err_host);
   cudaGetLastError();
   delete h;
   return MOE_OK;
@@ -841,23 +885,23 @@ moe_status moe_adapters_load(moe_adapters *h, int32_t slot, const void *a, const
   if (!dev.ok) return ad_fail(h, MOE_ERR_CUDA, "set device");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  // host sources pass through the staging buffer, in stream order
+  const void *src[2] = {a, b};
   bool host = false;
   for (int m = 0; m < 2 && rank && e == cudaSuccess; ++m) {
-    const int d = m ? g.d_out : g.d_in;
-    const void *src = m ? b : a;
-    if (host_ptr(src)) {  // both matrices pass through one buffer in stream order
-      host = true;
-      e = cudaMemcpyAsync(h->stage, src, static_cast<size_t>(rank) * d * 2, cudaMemcpyHostToDevice, st);
-      src = h->stage;
-      if (e != cudaSuccess) break;
-    }
-    const int64_t count = static_cast<int64_t>(round16(rank)) * ((d + 31) / 32 * 32);
-    k_adapter_pack<<<static_cast<unsigned>((count + 255) / 256), 256, 0, st>>>(
-        static_cast<const __nv_bfloat16 *>(src), m ? h->b + h->b_slot * slot : h->a + h->a_slot * slot, m, rank, d);
-    e = cudaGetLastError();
+    if (!host_ptr(src[m])) continue;
+    host = true;
+    __nv_bfloat16 *to = h->stage + (m ? static_cast<size_t>(g.d_in) * g.max_rank : 0);
+    e = cudaMemcpyAsync(to, src[m], static_cast<size_t>(rank) * (m ? g.d_out : g.d_in) * 2, cudaMemcpyHostToDevice, st);
+    src[m] = to;
   }
   if (e == cudaSuccess) {
-    k_adapter_meta<<<1, 1, 0, st>>>(h->meta + slot, AdMeta{rank, scale});
+    const int64_t r16 = round16(rank);
+    const int blocks_a = static_cast<int>((r16 * ((g.d_in + 31) / 32 * 32) + 255) / 256);
+    const int blocks_b = static_cast<int>((r16 * ((g.d_out + 31) / 32 * 32) + 255) / 256);
+    k_adapter_pack<<<rank ? blocks_a + blocks_b : 1, 256, 0, st>>>(
+        static_cast<const __nv_bfloat16 *>(src[0]), static_cast<const __nv_bfloat16 *>(src[1]), h->a + h->a_slot * slot,
+        h->b + h->b_slot * slot, h->meta + slot, AdMeta{rank, scale}, g.d_in, g.d_out, blocks_a);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && host) e = cudaStreamSynchronize(st);

@@ -196,7 +196,7 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * layer, so a quantised layer can be tuned against its original with the routed experts frozen).
  * All of them take device pointers, run on the current device (adapters: on their handle's),
  * enqueue on `stream`, never synchronise the host and allocate nothing, so they can be captured
- * into a CUDA graph.  Strides count values between the starts of consecutive rows.  Each result is
+ * into a CUDA graph (after a first call outside a capture, which loads and configures kernels).  Strides count values between the starts of consecutive rows.  Each result is
  * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
  * Outputs may not overlap inputs unless said so.
  * ------------------------------------------------------------------------------------------- */
@@ -310,7 +310,7 @@ const char *moe_adapters_last_error(const moe_adapters *h);
 uint64_t moe_adapters_device_bytes(const moe_adapters *h);
 
 /* Dense gated feed-forward block, bf16 weights: y = w_down (silu(w_gate x) * (w_up x)) (+ add).
- * d_model and d_ff: multiples of 8, 8..65536; every pointer 16-byte aligned, every row stride a
+ * n_tokens 1..1048576; d_model and d_ff: multiples of 8, 8..65536; every pointer 16-byte aligned, every row stride a
  * multiple of 16 bytes.  The hidden values are kept in bf16 between the products. */
 typedef struct {
   uint32_t struct_size;

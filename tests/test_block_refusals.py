@@ -77,7 +77,7 @@ FFN = dict(n_tokens=2, d_model=64, d_ff=32, x=64, w_gate=64, w_up=64, w_down=64,
            x_stride=64, y_stride=64)
 
 
-@pytest.mark.parametrize("bad", [dict(struct_size=4), dict(n_tokens=0), dict(d_model=60), dict(d_ff=12), dict(d_ff=0),
+@pytest.mark.parametrize("bad", [dict(struct_size=4), dict(n_tokens=0), dict(n_tokens=(1 << 20) + 1), dict(d_model=60), dict(d_ff=12), dict(d_ff=0),
                                  dict(d_model=65544), dict(x=None), dict(x=72), dict(w_gate=None), dict(w_up=None), dict(w_down=66),
                                  dict(y=None), dict(y_dtype=3), dict(x_stride=68), dict(x_stride=56), dict(add=64, add_stride=60),
                                  dict(add=64, add_stride=64, add_dtype=9), dict(save_gate=64), dict(workspace=None),

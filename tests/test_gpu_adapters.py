@@ -97,6 +97,25 @@ def test_one_adapter_runs_and_all_without(P):
     h.close()
 
 
+@pytest.mark.parametrize("xt,bt", [(BF, BF), (BF, F), (F, BF), (F, F)])
+@pytest.mark.parametrize("rank", [3, 32, 48, 128])
+def test_long_prompts(P, xt, bt, rank):
+    """Sizes of the widest tiles, in place too, ragged groups, some tokens without an adapter."""
+    n = 2500
+    h, a, b, sc = make(P, 264, 1032, [rank, max(1, rank - 5), 1], n, seed=6)
+    ids = (torch.randint(-1, 3, (n,), generator=rng(8)).sort().values).to(torch.int32).cuda()
+    x, base = data(n, 264, 1032, xt, bt)
+    out = h.apply(x, base, ids)
+    check(x, base, ids, a, b, sc, out, rank)
+    buf = base.clone()
+    h.apply(x, buf, ids, out=buf)
+    assert torch.equal(buf, out)
+    # the tokens' order is of no account
+    order = torch.randperm(n, generator=rng(9)).cuda()
+    assert torch.equal(h.apply(x[order].contiguous(), base[order].contiguous(), ids[order].contiguous()), out[order])
+    h.close()
+
+
 def test_many_slots_one_token_each(P):
     n = 300
     h, a, b, sc = make(P, 128, 128, [1 + i % 20 for i in range(n)], 512)

@@ -87,6 +87,25 @@ def test_backward(P, n, d, f):
     assert part[0] is None and all(torch.equal(a, b) for a, b in zip(part[1:], got[1:]))
 
 
+@pytest.mark.parametrize("n", [3, 8, 12, 40, 130, 300])
+@pytest.mark.parametrize("d,f", [(512, 8192), (200, 4104)])
+def test_long_products_of_few_tokens(P, n, d, f):
+    """The down product and dx run over many more values than they have results."""
+    w = weights(d, f)
+    x, dy = randn(n, d, seed=5), randn(n, d, seed=6, std=0.1)
+    r = R.ffn(x, *w, dy)
+    add = randn(n, d, seed=7, dtype=F)
+    for kw in ({}, {"add": add, "out_dtype": F}, {"add": add.to(BF)}):
+        y = P.ffn_forward(x, *w, **kw)
+        check_y(y, r, w[2], kw.get("add"))
+        assert torch.equal(y, P.ffn_forward(x, *w, **kw))
+    _, saved = P.ffn_forward(x, *w, save=True)
+    got = P.ffn_backward(dy, x, *w, saved)
+    check_gradients(got, x, w, dy, r)
+    assert torch.equal(P.ffn_backward(dy, x, *w, saved, need_dw=False)[0], got[0])
+    assert torch.equal(P.ffn_backward(dy, x, *w, saved, need_dx=False)[3], got[3])
+
+
 def test_large(P):
     n, d, f = 2500, 2048, 2304
     w = weights(d, f)
