@@ -586,7 +586,13 @@ __global__ void __launch_bounds__(1024) k_adapter_group(AdArgs a, int4 *tiles, i
     __syncthreads();
     int r0 = s_base[0] + sr - c, t0 = s_base[1] + st - nt;
     for (int w = 0; w < warp; ++w) r0 += s_rows[w], t0 += s_tiles[w];
-    for (int k = 0; k < nt; ++k) tiles[t0 + k] = make_int4(r0 + k * tm, min(tm, c - k * tm), i, 0);
+    // few tiles: the group's thread writes them; many: the whole warp, one group after the other
+    for (int k = 0; k < nt && nt <= 8; ++k) tiles[t0 + k] = make_int4(r0 + k * tm, min(tm, c - k * tm), i, 0);
+    for (uint32_t some = __ballot_sync(0xffffffffu, nt > 8); some; some &= some - 1) {
+      const int from = __ffs(some) - 1, n1 = __shfl_sync(0xffffffffu, nt, from), t1 = __shfl_sync(0xffffffffu, t0, from);
+      const int r1 = __shfl_sync(0xffffffffu, r0, from), c1 = __shfl_sync(0xffffffffu, c, from), i1 = i - lane + from;
+      for (int k = lane; k < n1; k += 32) tiles[t1 + k] = make_int4(r1 + k * tm, min(tm, c1 - k * tm), i1, 0);
+    }
     if (i < groups) s_cnt[i] = r0;
     __syncthreads();
     if (tid == 1023) s_base[0] = r0 + c, s_base[1] = t0 + nt;

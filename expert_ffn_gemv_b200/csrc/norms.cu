@@ -256,6 +256,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd(const __grid_const
   __shared__ __align__(16) float red[16];
   const int64_t t = blockIdx.x;
   const int d = a.d;
+  griddep_wait();
+  griddep_launch();
   float r[NCH][V], o[NCH][V], g[NCH][V], w[NCH][V], wn[NCH][V];
   fill<V, NCH>(r, 0.f), fill<V, NCH>(o, 0.f), fill<V, NCH>(g, 0.f), fill<V, NCH>(w, 0.f), fill<V, NCH>(wn, 0.f);
   load_row<V, NCH>(a.res, t * a.res_ld, a.res_bf16, d, r);
@@ -359,6 +361,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_norm_bwd(const __grid_const
   __shared__ __align__(16) float red[48];
   const int d = a.d, threads = blockDim.x;
   clear_sums(red);
+  griddep_wait();
+  griddep_launch();
   constexpr bool KEEP = V * NCH <= 16;
   BwdState<V, NCH, KEEP> st(a);
   auto load = [&](int64_t t, BwdRow<V, NCH> &q, float &gt) {
@@ -483,6 +487,8 @@ __global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 3 : NCH == 2 ? 2 : 1)
   const int d = a.d;
   RingState ring(smem, r);
   clear_sums(red);
+  griddep_wait();
+  griddep_launch();
   if (ring.producer()) {
     ring.produce(r, d, n);
     return;
@@ -533,6 +539,8 @@ __global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 2 : 1) k_norm_bwd_rin
   const int d = a.d;
   RingState ring(smem, r);
   clear_sums(red);
+  griddep_wait();
+  griddep_launch();
   if (ring.producer()) {
     ring.produce(r, d, a.n);
     return;
@@ -561,8 +569,8 @@ __global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 2 : 1) k_norm_bwd_rin
   st.finish(a);
 }
 
-// out[i] = sum over rows of part[row][i]: 32 threads a column add every 32nd row in order, their sums
-// are added in order; blockIdx.y picks one of two sums.
+// out[i] = sum over rows of part[row][i]: warp y of a block adds every 32nd row of 32 columns in order,
+// then one warp a column adds the 32 sums in a fixed tree; blockIdx.y picks one of two sums.
 struct ColSum {
   const float *part[2];
   void *out[2];
@@ -571,20 +579,24 @@ struct ColSum {
 };
 __global__ void __launch_bounds__(1024) k_colsum(ColSum a) {
   __shared__ float s[32][33];
-  const int which = blockIdx.y, i = blockIdx.x * 32 + threadIdx.x;
-  const float *part = a.part[which] + i;
+  const int which = blockIdx.y, x = threadIdx.x, y = threadIdx.y, i = blockIdx.x * 32 + x;
+  griddep_wait();
+  griddep_launch();
+  const float *part = a.part[which] + static_cast<int64_t>(y) * a.d + i;
   float v = 0.f;
   if (i < a.d) {
-#pragma unroll 8
-    for (int r = threadIdx.y; r < a.rows; r += 32) v += part[static_cast<int64_t>(r) * a.d];
+#pragma unroll 16
+    for (int r = y; r < a.rows; r += 32, part += 32 * static_cast<int64_t>(a.d)) v += *part;
   }
-  s[threadIdx.y][threadIdx.x] = v;
+  s[y][x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && i < a.d) {
+  v = s[x][y];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) v += s[k][threadIdx.x];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + y;
+  if (x == 0 && col < a.d) {
     float o[1] = {v};
-    store_v<1>(a.out[which], i, a.bf16[which], o);
+    store_v<1>(a.out[which], col, a.bf16[which], o);
   }
 }
 
@@ -606,6 +618,23 @@ int norm_threads(int d, int v) {
 }
 
 // Calls f with the instantiation that holds a row of d <= kNormMaxD values, v at a time.
+// Launch with programmatic stream serialization: a kernel may begin while the one before it ends, and
+// waits for its results itself.
+template <typename... P>
+void launch(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, const P &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);  // an error is the last error, which the callers read
+}
+
 template <typename F>
 cudaError_t pick_norm(int d, int v, F f) {
   const int threads = norm_threads(d, v), nch = (d + v * threads - 1) / (v * threads);
@@ -709,10 +738,10 @@ moe_status launch_fwd(const NormFwd &a, int n, int v, cudaStream_t st) {
   if (e == cudaSuccess && p.r.stages) {
     e = configure_rings();
     if (e == cudaSuccess)
-      e = pick_ring<4>(a.d, [&](auto nch) { k_norm_fwd_ring<decltype(nch)::value><<<p.blocks, p.threads + 32, p.smem, st>>>(a, p.r, n); });
+      e = pick_ring<4>(a.d, [&](auto nch) { launch(k_norm_fwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, a, p.r, n); });
   } else if (e == cudaSuccess) {
     e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
-      k_norm_fwd<decltype(vv)::value, decltype(nch)::value><<<n, threads, 0, st>>>(a);
+      launch(k_norm_fwd<decltype(vv)::value, decltype(nch)::value>, n, threads, 0, st, a);
     });
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -755,14 +784,14 @@ moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf
   if (p.r.stages) {
     e = configure_rings();
     if (e == cudaSuccess)
-      e = pick_ring<2>(a.d, [&](auto nch) { k_norm_bwd_ring<decltype(nch)::value><<<p.blocks, p.threads + 32, p.smem, st>>>(a, p.r); });
+      e = pick_ring<2>(a.d, [&](auto nch) { launch(k_norm_bwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, static_cast<const NormBwd &>(a), p.r); });
   } else {
     e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
-      k_norm_bwd<decltype(vv)::value, decltype(nch)::value><<<blocks, threads, 0, st>>>(a);
+      launch(k_norm_bwd<decltype(vv)::value, decltype(nch)::value>, blocks, threads, 0, st, static_cast<const NormBwd &>(a));
     });
   }
   if (e == cudaSuccess && sums) {
-    k_colsum<<<dim3((a.d + 31) / 32, sums), dim3(32, 32), 0, st>>>(c);
+    launch(k_colsum, dim3((a.d + 31) / 32, sums), dim3(32, 32), 0, st, c);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
