@@ -592,11 +592,12 @@ __global__ void __launch_bounds__(256) k_ffn_sum(SumArgs a) {
 // on both sides, so it does not matter), the tokens as the 8-column operand.  A cluster of CL blocks
 // has 16 rows; its blocks take runs of k, their warps interleaved pieces of 64 k (128 bytes of a row);
 // the sums meet in shared memory, then over the cluster, and are added in warp and block order.
-// Bound by the weights' bytes: what counts is loads on their way, so there are four or more blocks an
-// SM and eight weight loads a lane (8 tokens, d 2,048, f 8,192: one block an SM in the down product
-// gave 1.3 TB/s, with clusters of four).
+// Bound by the weights' bytes: what counts is loads on their way, so there are up to eight small blocks
+// an SM and eight weight loads a lane.  8 tokens, d 2,048, f 8,192 (100 MB of weights): 29 us, 3.4 TB/s;
+// with one block an SM in the down product 41, with four blocks of eight warps 31, with twelve of four
+// warps and half the loads 30, with two persistent blocks fed by cp.async 38.
 // ------------------------------------------------------------------------------------------
-constexpr int kSmThreads = 256, kSmWarps = 8;
+constexpr int kSmThreads = 128, kSmWarps = 4;
 constexpr int kSmallMax = 8;  // tokens: the MMA's columns (16 in two column groups took 38 us, in k_ffn_gemm 35)
 
 struct SmallArgs {
@@ -689,7 +690,7 @@ __device__ __forceinline__ bool small_product(const __nv_bfloat16 *r0, const __n
 
 // Cluster: 8 rows of Wg (operand rows 0..7) and the same 8 of Wu (8..15): a lane gets g and u of the
 // same row and tokens.
-__global__ void __launch_bounds__(kSmThreads, 4) k_ffn_up(SmallArgs a, int cl) {
+__global__ void __launch_bounds__(kSmThreads, 8) k_ffn_up(SmallArgs a, int cl) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, row = blockIdx.x / cl * 8 + g;
   float acc[4] = {};
   const bool ok = row < a.f;
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) k_ffn_up(SmallArgs a, int cl) {
 
 // Cluster: 16 rows of Wd.  Launched while k_ffn_up ends (which began when everything before it had
 // completed), it has weights on their way before it waits for h.
-__global__ void __launch_bounds__(kSmThreads, 4) k_ffn_down(SmallArgs a, int cl) {
+__global__ void __launch_bounds__(kSmThreads, 8) k_ffn_down(SmallArgs a, int cl) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, r0 = blockIdx.x / cl * 16 + g, r1 = r0 + 8;
   float acc[4] = {};
   const bool mine = small_product(a.wd + static_cast<int64_t>(r0) * a.f, a.wd + static_cast<int64_t>(r1) * a.f, r0 < a.d, r1 < a.d,
@@ -882,7 +883,7 @@ cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
 }
 
 // Blocks of a cluster over k: enough clusters x blocks for four an SM, each of eight pieces of 64 at
-// least (one for every warp).
+// least (two for every warp; with one, 2,048 x 768 takes 9.6 us in place of 8.3).
 int small_cluster(int tiles, int k) {
   int cl = 1;
   while (cl < 8 && tiles * cl < 4 * 148 && (k + 63) / 64 >= 16 * cl) cl *= 2;
