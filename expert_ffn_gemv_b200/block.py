@@ -122,8 +122,8 @@ def norm_out_backward(o, d_res, *, weight=None, eps=1e-6, unit_offset=False, gat
 # --------------------------------------------------------------------------------------- adapters
 class Adapters:
     """Low-rank adapters of many requests beside a shared projection or block (``moe_adapters_*``):
-    out_t = base_t + scale_i B_i (A_i x_t), i = ids[t]; -1: no adapter.  One handle serves one stream at
-    a time."""
+    out_t = base_t + scale_i B_i (A_i x_t), i = ids[t]; -1: no adapter.  Calls of ``apply`` may run at once
+    on several streams and in captured graphs."""
 
     def __init__(self, *, d_in, d_out, max_adapters, max_rank, max_tokens=8, device=0):
         self.h = None

@@ -36,7 +36,7 @@ constexpr int kAdMaxRank = 128;
 constexpr int kAdMaxTokens = 8192;
 constexpr int kAdMaxSlots = 4096;
 constexpr int kAdMaxD = 65536;
-constexpr int kAdInKernel = 256;    // up to this many tokens every block groups the ids itself
+constexpr int kAdInKernel = 256;    // up to this many tokens ids are compared with one another, beyond counted
 constexpr int kAdGroups = 8;        // n8 rank groups of one pass over x: 64 ranks
 constexpr int kRedLd = 8 * kAdGroups + 8;
 constexpr uint64_t kAdSpin = 2000000000ull;  // about a second
@@ -58,9 +58,6 @@ struct AdArgs {
   const int *ids;
   const __nv_bfloat16 *a, *b;  // packed, slot strides a_slot / b_slot (elements)
   const AdMeta *meta;
-  const int4 *tiles;           // more than kAdInKernel tokens: first place in order, tokens, adapter
-  const int *order;            // tokens grouped by adapter
-  const int *n_tiles;
   uint32_t *err;
   int64_t x_ld, base_ld, out_ld, a_slot, b_slot;
   int n, d_in, d_out, slots, max_rank16;
@@ -108,16 +105,12 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// The adapter a token asks for: slots stands for "none" (id -1), and for ids out of range or of a
-// slot that is not loaded, which raise the error word.
-__device__ __forceinline__ int ad_id(const AdArgs &a, int t, bool report) {
-  const int id = a.ids[t];
-  if (id == -1) return a.slots;
-  if (id < 0 || id >= a.slots || a.meta[id].rank == 0) {
-    if (report) flag_error(a.err, kErrBadIndex);
-    return a.slots;
-  }
-  return id;
+// The adapter a token asks for: slots stands for "none" (id -1), and for ids out of range, which raise
+// the error word.  (Whether the slot is loaded is seen once a tile.)
+__device__ __forceinline__ int ad_id(const AdArgs &a, int id, bool report) {
+  const bool in = id >= 0 && id < a.slots;
+  if (!in && id != -1 && report) flag_error(a.err, kErrBadIndex);
+  return in ? id : a.slots;
 }
 
 // Few tokens: finds tile `want` of the grouped order and writes its tokens to rows[]; every block
@@ -128,7 +121,7 @@ __device__ int ad_find_tile(const AdArgs &a, int want, bool report, int *rows, i
   __shared__ int s_id[kAdInKernel], s_warp[kAdWarps + 1], s_got[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int id = -1;
-  if (tid < a.n) id = ad_id(a, tid, report);
+  if (tid < a.n) id = ad_id(a, a.ids[tid], report);
   if (tid < kAdInKernel) s_id[tid] = id;
   if (tid < 2) s_got[tid] = 0;
   __syncthreads();
@@ -168,6 +161,83 @@ __device__ int ad_find_tile(const AdArgs &a, int want, bool report, int *rows, i
   }
   __syncthreads();
   return s_got[0];
+}
+
+// Many tokens: the same, with the tiles numbered by slot (the tokens without an adapter last).  Every
+// block counts the ids of all tokens for itself (counters and the ids it read in `scratch`): reading
+// them takes less time than a launch that would sort them for all, and a call needs no workspace.
+template <int TM>
+__device__ int ad_find_tile_many(const AdArgs &a, int want, bool report, unsigned char *scratch, int *rows, int &adapter) {
+  __shared__ int s_warp[kAdWarps], s_sel[3], s_base;
+  int *count = reinterpret_cast<int *>(scratch);                                 // [slots + 1]
+  uint16_t *ids = reinterpret_cast<uint16_t *>(scratch + (kAdMaxSlots + 64) * 4);  // [n]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = a.slots + 1;
+  for (int i = tid; i < groups; i += kAdBlock) count[i] = 0;
+  if (tid == 0) s_base = 0, s_sel[0] = -1;
+  __syncthreads();
+  // warp w has tokens w * each .. of a run; a warp's lanes with the same id make one atomic (a few long
+  // prompts put every token on one counter)
+  const int each = (a.n + 32 * kAdWarps - 1) / (32 * kAdWarps) * 32, t0 = warp * each;
+  if (warp < kAdWarps)
+    for (int b = t0 + lane; b < t0 + each; b += 8 * 32) {  // eight loads on their way
+      int id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) id[k] = __ldg(a.ids + min(b + 32 * k, a.n - 1));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int t = b + 32 * k;
+        id[k] = t < t0 + each && t < a.n ? ad_id(a, id[k], report) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (id[k] >= 0) ids[b + 32 * k] = static_cast<uint16_t>(id[k]);
+        const uint32_t same = __match_any_sync(0xffffffffu, id[k]);
+        if (id[k] >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[id[k]], __popc(same));
+      }
+    }
+  __syncthreads();
+  for (int i0 = 0; i0 < groups; i0 += kAdThreads) {
+    const int i = i0 + tid, c = tid < kAdThreads && i < groups ? count[i] : 0;
+    const int nt = i == a.slots && a.in_place ? 0 : (c + TM - 1) / TM;
+    int scan = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31 && warp < kAdWarps) s_warp[warp] = scan;
+    __syncthreads();
+    int first = s_base + scan - nt;
+    for (int w = 0; w < warp && w < kAdWarps; ++w) first += s_warp[w];
+    if (nt && want >= first && want < first + nt) s_sel[0] = i, s_sel[1] = (want - first) * TM, s_sel[2] = c;
+    __syncthreads();
+    if (tid == kAdThreads - 1) s_base = first + nt;
+    __syncthreads();
+    if (s_sel[0] >= 0) break;
+  }
+  adapter = s_sel[0];
+  if (adapter < 0) return 0;
+  // the tile's tokens: places lo .. of the adapter's tokens in their order
+  int mine = 0;
+  if (warp < kAdWarps)
+#pragma unroll 8
+    for (int t = t0 + lane; t < t0 + each; t += 32) mine += __popc(__ballot_sync(0xffffffffu, t < a.n && ids[t] == adapter));
+  if (lane == 0 && warp < kAdWarps) s_warp[warp] = mine;
+  __syncthreads();
+  const int lo = s_sel[1];
+  if (warp < kAdWarps) {
+    int at = -lo;
+    for (int w = 0; w < warp; ++w) at += s_warp[w];
+    for (int t = t0 + lane; t < t0 + each && at < TM; t += 32) {
+      const bool is = t < a.n && ids[t] == adapter;
+      const uint32_t all = __ballot_sync(0xffffffffu, is);
+      const int place = at + __popc(all & ((1u << lane) - 1u));
+      if (is && place >= 0 && place < TM) rows[place] = t;
+      at += __popc(all);
+    }
+  }
+  __syncthreads();
+  return min(TM, s_sel[2] - lo);
 }
 
 // 16 bytes to this thread's slot; zeros where there is no source
@@ -413,20 +483,16 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
   griddep_launch();
 
   int adapter, cnt;
-  if (a.n <= kAdInKernel) {
+  if (a.n <= kAdInKernel)
     cnt = ad_find_tile<TM>(a, tile, blockIdx.x == 0, rows, adapter);
-  } else {
-    cnt = 0, adapter = -1;
-    if (tile < *a.n_tiles) {
-      const int4 ti = a.tiles[tile];
-      cnt = ti.y, adapter = ti.z;
-      if (tid < cnt) rows[tid] = a.order[ti.x + tid];
-    }
-    __syncthreads();
-  }
+  else
+    cnt = ad_find_tile_many<TM>(a, tile, blockIdx.x == 0, smem + S.ring, rows, adapter);
   if (cnt == 0) return;  // the same for every block of the cluster
   AdMeta meta{0, 0.f};
-  if (adapter < a.slots) meta = a.meta[adapter];
+  if (adapter < a.slots) {
+    meta = a.meta[adapter];
+    if (meta.rank == 0 && cr == 0 && tid == 0) flag_error(a.err, kErrBadIndex);  // the slot is empty: as none
+  }
   const int r16 = round16(meta.rank), ng = r16 / 8, nk = r16 / 16;
   const int kb_all = (a.d_in + 31) / 32, kb0 = kb_all * cr / cl, kb1 = kb_all * (cr + 1) / cl;
   const int nb_all = (a.d_out + 31) / 32, nb0 = nb_all * cr / cl, nb1 = nb_all * (cr + 1) / cl;
@@ -535,76 +601,12 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
   const uint32_t vaddr = smem_u32(smem + S.v) + ((16 * mg + (l.lane & 15)) * S.v_ld + (l.lane >> 4) * 8) * 2;
   if (nk)
     ad_expand<KG, XP, VP, RC>(l, br, orow, nb0 + kg, nb1, a.d_out, ring, nk, vaddr, S.v_part, limit, a.err);
+  else if (a.in_place)
+    ad_wait_all();
   else
     ad_plain_rows<KG, IO>(l, orow, nb0 + kg, nb1, a.d_out, br);
   __syncwarp();
   if (cl > 1) cluster_wait();
-}
-
-// Takes the next place of counter id (ids below 0: none): one atomic for all of a warp's lanes with the
-// same id (a few long prompts put every lane on one counter: 15 us for 8,192 tokens without this).
-__device__ __forceinline__ int ad_take(int *counters, int id) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t same = __match_any_sync(0xffffffffu, id);
-  const int leader = __ffs(same) - 1;
-  int at = 0;
-  if (lane == leader && id >= 0) at = atomicAdd(&counters[id], __popc(same));
-  at = __shfl_sync(0xffffffffu, at, leader);
-  return at + __popc(same & ((1u << lane) - 1u));
-}
-
-// Counting sort of the tokens by adapter and the list of tiles (more than kAdInKernel tokens); one
-// block.  The order inside a group is the order of arrival, which no result depends on: every row
-// is computed by itself.
-__global__ void __launch_bounds__(1024) k_adapter_group(AdArgs a, int4 *tiles, int *order, int *n_tiles, int tm) {
-  extern __shared__ int s_cnt[];  // [slots + 1] counts, then cursors
-  __shared__ int s_rows[32], s_tiles[32], s_base[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = a.slots + 1;
-  constexpr int kEach = kAdMaxTokens / 1024;
-  for (int i = tid; i < groups; i += 1024) s_cnt[i] = 0;
-  if (tid < 2) s_base[tid] = 0;
-  griddep_wait();
-  griddep_launch();
-  int id[kEach];
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) id[k] = tid + 1024 * k < a.n ? ad_id(a, tid + 1024 * k, true) : -1;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kEach; ++k)
-    if (1024 * k < a.n) ad_take(s_cnt, id[k]);
-  __syncthreads();
-  for (int i0 = 0; i0 < groups; i0 += 1024) {
-    const int i = i0 + tid, c = i < groups ? s_cnt[i] : 0;
-    const int nt = i == a.slots && a.in_place ? 0 : (c + tm - 1) / tm;
-    int sr = c, st = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, sr, o), v = __shfl_up_sync(0xffffffffu, st, o);
-      if (lane >= o) sr += u, st += v;
-    }
-    if (lane == 31) s_rows[warp] = sr, s_tiles[warp] = st;
-    __syncthreads();
-    int r0 = s_base[0] + sr - c, t0 = s_base[1] + st - nt;
-    for (int w = 0; w < warp; ++w) r0 += s_rows[w], t0 += s_tiles[w];
-    // few tiles: the group's thread writes them; many: the whole warp, one group after the other
-    for (int k = 0; k < nt && nt <= 8; ++k) tiles[t0 + k] = make_int4(r0 + k * tm, min(tm, c - k * tm), i, 0);
-    for (uint32_t some = __ballot_sync(0xffffffffu, nt > 8); some; some &= some - 1) {
-      const int from = __ffs(some) - 1, n1 = __shfl_sync(0xffffffffu, nt, from), t1 = __shfl_sync(0xffffffffu, t0, from);
-      const int r1 = __shfl_sync(0xffffffffu, r0, from), c1 = __shfl_sync(0xffffffffu, c, from), i1 = i - lane + from;
-      for (int k = lane; k < n1; k += 32) tiles[t1 + k] = make_int4(r1 + k * tm, min(tm, c1 - k * tm), i1, 0);
-    }
-    if (i < groups) s_cnt[i] = r0;
-    __syncthreads();
-    if (tid == 1023) s_base[0] = r0 + c, s_base[1] = t0 + nt;
-    __syncthreads();
-  }
-  if (tid == 0) *n_tiles = s_base[1];
-#pragma unroll
-  for (int k = 0; k < kEach; ++k)
-    if (1024 * k < a.n) {
-      const int at = ad_take(s_cnt, id[k]);
-      if (id[k] >= 0) order[at] = tid + 1024 * k;
-    }
 }
 
 // A (rank x d_in) and B (d_out x rank) into the kernels' operand order, padded with zeros to 16
@@ -695,8 +697,6 @@ struct moe_adapters {
   void *mem = nullptr;
   __nv_bfloat16 *a = nullptr, *b = nullptr, *stage = nullptr;
   AdMeta *meta = nullptr;
-  int4 *tiles = nullptr;
-  int *order = nullptr, *n_tiles = nullptr;
   uint32_t *err_host = nullptr, *err_dev = nullptr;
   std::string last_error;
 };
@@ -829,7 +829,6 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
   };
   const uint64_t oa = take(h->a_slot * 2 * g.max_adapters), ob = take(h->b_slot * 2 * g.max_adapters);
   const uint64_t os = take((static_cast<uint64_t>(g.d_in) + g.d_out) * g.max_rank * 2), om = take(sizeof(AdMeta) * g.max_adapters);
-  const uint64_t ot = take(16 * (g.max_tokens / 16 + g.max_adapters + 2)), oo = take(4ull * g.max_tokens), on = take(4);
   cudaError_t e = cudaMalloc(&h->mem, off);
   moe_status s = MOE_OK;
   if (e != cudaSuccess) {
@@ -842,9 +841,6 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
     h->b = reinterpret_cast<__nv_bfloat16 *>(p + ob);
     h->stage = reinterpret_cast<__nv_bfloat16 *>(p + os);
     h->meta = reinterpret_cast<AdMeta *>(p + om);
-    h->tiles = reinterpret_cast<int4 *>(p + ot);
-    h->order = reinterpret_cast<int *>(p + oo);
-    h->n_tiles = reinterpret_cast<int *>(p + on);
     e = cudaMemset(h->meta, 0, sizeof(AdMeta) * g.max_adapters);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) {
@@ -937,7 +933,7 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   AdArgs a{};
   a.x = x, a.base = base, a.out = out, a.ids = ids;
   a.a = h->a, a.b = h->b, a.meta = h->meta, a.a_slot = h->a_slot, a.b_slot = h->b_slot;
-  a.tiles = h->tiles, a.order = h->order, a.n_tiles = h->n_tiles, a.err = h->err_dev;
+  a.err = h->err_dev;
   a.x_ld = x_stride, a.base_ld = base_stride, a.out_ld = out_stride;
   a.n = n_tokens, a.d_in = g.d_in, a.d_out = g.d_out, a.slots = g.max_adapters, a.max_rank16 = h->r16;
   a.x_bf16 = x_dtype == MOE_BF16, a.io_bf16 = out_dtype == MOE_BF16;
@@ -945,10 +941,6 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   const int tm = tile_rows(n_tokens);
   const int64_t tiles = most_tiles(n_tokens, tm, g.max_adapters);
   cudaError_t e = cudaSuccess;
-  if (n_tokens > kAdInKernel) {
-    const AdConfig c(1, 1024, (g.max_adapters + 1) * 4, 1, st);
-    e = cudaLaunchKernelEx(&c.cfg, k_adapter_group, a, h->tiles, h->order, h->n_tiles, tm);
-  }
   int cl = 8;
   while (cl > 1 && tiles * cl > 2 * h->nsm) cl >>= 1;
   if (e == cudaSuccess)

@@ -279,15 +279,16 @@ typedef struct {
 moe_status moe_norm_out_backward(const moe_norm_out_bwd_args *args, void *stream);
 
 /* Low-rank adapters of many requests:  out_t = base_t + scale_i B_i (A_i x_t) with i = ids[t], and
- * out_t = base_t where ids[t] = -1.  The handle owns the adapters (repacked) and a workspace; like
- * a moe_handle it serves one stream at a time, captured graphs included. */
+ * out_t = base_t where ids[t] = -1.  The handle owns the adapters (repacked).  moe_adapters_apply
+ * writes nothing but out, so calls of one handle may run at once on several streams and in captured
+ * graphs; a load is ordered by its stream, and loads are made one at a time. */
 typedef struct moe_adapters moe_adapters; /* opaque */
 typedef struct {
   uint32_t struct_size;   /* sizeof(moe_adapters_config) */
   int32_t d_in, d_out;    /* multiples of 8, 8..65536 */
   int32_t max_adapters;   /* slots, 1..4096 */
   int32_t max_rank;       /* 1..128 */
-  int32_t max_tokens;     /* per call, 1..8192 */
+  int32_t max_tokens;     /* largest n_tokens per call, 1..8192 */
   int32_t device;
 } moe_adapters_config;
 moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **out);

@@ -224,6 +224,37 @@ def test_graph_and_stream(P, n):
     h.close()
 
 
+def test_two_streams_and_two_graphs_at_once(P):
+    """Nothing of a call is kept in the handle: calls may overlap."""
+    n = 700
+    h, a, b, sc = make(P, 512, 512, [16, 48, 5], n)
+    sets = []
+    for k in range(2):
+        x, base = data(n, 512, 512, BF, F, seed=20 + k)
+        ids = torch.randint(-1, 3, (n,), generator=rng(30 + k)).to(torch.int32).cuda()
+        sets.append((x, base, ids, h.apply(x, base, ids)))
+    streams = [torch.cuda.Stream() for _ in sets]
+    graphs, outs = [], []
+    for s, (x, base, ids, _) in zip(streams, sets):
+        s.wait_stream(torch.cuda.current_stream())
+        g, out = torch.cuda.CUDAGraph(), torch.empty_like(base)
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(20):
+                h.apply(x, base, ids, out=out)
+        graphs.append(g), outs.append(out)
+    torch.cuda.synchronize()
+    for s, g in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            g.replay()
+    for s, (x, base, ids, _), out in zip(streams, sets, outs):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                h.apply(x, base, ids, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[3]) for o, want in zip(outs, sets))
+    h.close()
+
+
 def test_refusals(P):
     h, *_ = make(P, 64, 64, [4], 16)
     x, base = data(4, 64, 64, BF, BF)
