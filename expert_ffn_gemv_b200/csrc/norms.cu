@@ -9,6 +9,10 @@
 //   t = dz a w       do = q (t - o q^2 mean(t o))       dw += dz a o q      dg = dz u a'(g)
 // Backward of the input norm:
 //   t = dh w'        dr = dr' + p (t - x p^2 mean(t x))  dw' += dh x p
+// The products and sums that decide a stored value's last bits are rounded in the order written above,
+// without fused multiply-adds: where a residual or gradient is then rounded to bf16 it falls on the side
+// that the formula's fp32 evaluation gives, so that what is computed from it in fp32 (dw, do, dw') agrees
+// to 2e-5.  With them contracted, one gradient in sixteen over random shapes was further off.
 // Sums over columns are taken over the row's threads (shuffles, then the warps in order), sums over
 // tokens (dw, the gradient of a channel gate) in two steps: every block of a grid that depends on the
 // device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No atomics:
@@ -173,15 +177,23 @@ __device__ __forceinline__ void clear_sums(float (&red)[N]) {
   __syncthreads();
 }
 
+// a(g).  A gate of a row scales all its values, so that its last bit decides many roundings: it is taken
+// with expf and a division.  Gates by the value take the approximate forms, 3 units in the last place off
+// (8,192 x 4,096, a gate for every value: 55 us, 69 with the others).
 __device__ __forceinline__ float gate_value(float g, int act) {
-  if (act != MOE_GATE_SIGMOID) return g;
-  float r;  // approximate reciprocal (1 ulp; of infinity: 0): an IEEE division takes ten instructions
+  return act == MOE_GATE_SIGMOID ? 1.0f / (1.0f + expf(-g)) : g;
+}
+__device__ __forceinline__ float gate_value_fast(float g) {
+  float r;  // (of infinity: 0)
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
   return r;
 }
+// 1 / sqrt(sum / d + eps)
+__device__ __forceinline__ float root(float sum, float inv_d, float eps) { return rsqrtf(__fadd_rn(__fmul_rn(sum, inv_d), eps)); }
+
 template <int V, int NCH>
 __device__ __forceinline__ void gate_values(float (&g)[NCH][V], int act) {
-  if (act == MOE_GATE_SIGMOID) MOE_EACH(c, k) g[c][k] = gate_value(g[c][k], MOE_GATE_SIGMOID);
+  if (act == MOE_GATE_SIGMOID) MOE_EACH(c, k) g[c][k] = gate_value_fast(g[c][k]);
 }
 
 struct NormFwd {
@@ -215,20 +227,19 @@ __device__ __forceinline__ void fwd_row(const NormFwd &a, int64_t t, float (&r)[
   const int d = a.d;
   if (a.o) {
     const bool by_value = gate_by_value(a.gate_kind);
-    const float f = a.scale * gt;
     if (a.w) {
       float ss[1] = {0.f};
       MOE_EACH(c, k) ss[0] = fmaf(o[c][k], o[c][k], ss[0]);
       if (!KEEP) load_weight<V, NCH>(a.w, a.w_bf16, d, a.w_off, w);
       block_sum<1>(ss, red, threads);
-      const float q = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
-      MOE_EACH(c, k) o[c][k] *= q * w[c][k];
+      const float q = root(ss[0], a.inv_d, a.eps);
+      MOE_EACH(c, k) o[c][k] = __fmul_rn(__fmul_rn(o[c][k], q), w[c][k]);
     }
     if (by_value) {
       if (!active) gate_values<V, NCH>(g, a.gate_act);
-      MOE_EACH(c, k) r[c][k] = fmaf(f * g[c][k], o[c][k], r[c][k]);
+      MOE_EACH(c, k) r[c][k] = __fadd_rn(r[c][k], __fmul_rn(a.scale, __fmul_rn(g[c][k], o[c][k])));
     } else {
-      MOE_EACH(c, k) r[c][k] = fmaf(f, o[c][k], r[c][k]);
+      MOE_EACH(c, k) r[c][k] = __fadd_rn(r[c][k], __fmul_rn(a.scale, __fmul_rn(gt, o[c][k])));
     }
     store_row<V, NCH>(a.res_out, t * a.out_ld, a.out_bf16, d, r);
   }
@@ -237,8 +248,8 @@ __device__ __forceinline__ void fwd_row(const NormFwd &a, int64_t t, float (&r)[
   MOE_EACH(c, k) ss[0] = fmaf(r[c][k], r[c][k], ss[0]);
   if (!KEEP) load_weight<V, NCH>(a.next_w, a.w_bf16, d, a.w_off, wn);
   block_sum<1>(ss, red + 8, threads);
-  const float p = rsqrtf(fmaf(ss[0], a.inv_d, a.next_eps));
-  MOE_EACH(c, k) r[c][k] *= p * wn[c][k];
+  const float p = root(ss[0], a.inv_d, a.next_eps);
+  MOE_EACH(c, k) r[c][k] = __fmul_rn(__fmul_rn(r[c][k], p), wn[c][k]);
   store_row<V, NCH>(a.h, t * a.h_ld, a.h_bf16, d, r);
 }
 
@@ -317,35 +328,42 @@ __device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, N
     gate_values<V, NCH>(q.g, a.gate_act);
   } else if (channel) {
     MOE_EACH(c, k) q.g[c][k] = st.gc[c][k];
-  } else {
-    fill<V, NCH>(q.g, gt);
   }
-  // sums of x^2, of (dy a w) x and of dy x w (the token gate's gradient), without their common
-  // factors s and q
-  float s[3] = {0.f, 0.f, 0.f};
+  // sums of x^2 and of s dy a w x, the second without the gate where a row has only one
+  const bool by_value = full || channel;
+  float s[2] = {0.f, 0.f};
   MOE_EACH(c, k) {
-    const float e = q.dy[c][k] * q.x[c][k] * st.w[c][k];
+    q.dy[c][k] = __fmul_rn(a.scale, q.dy[c][k]);
     s[0] = fmaf(q.x[c][k], q.x[c][k], s[0]);
-    s[1] = fmaf(e, q.g[c][k], s[1]);
-    s[2] += e;
   }
-  block_sum<3>(s, red, threads);
-  const float root = a.w ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 1.f;
-  const float m = a.w ? a.scale * root * root * root * (s[1] * a.inv_d) : 0.f, sr = a.scale * root;
-  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID, want_dg = full || channel;
+  if (by_value) {
+    MOE_EACH(c, k) s[1] = fmaf(__fmul_rn(__fmul_rn(q.dy[c][k], q.g[c][k]), st.w[c][k]), q.x[c][k], s[1]);
+  } else {
+    MOE_EACH(c, k) s[1] = fmaf(__fmul_rn(q.dy[c][k], st.w[c][k]), q.x[c][k], s[1]);
+  }
+  block_sum<2>(s, red, threads);
+  const float rt = a.w ? root(s[0], a.inv_d, a.eps) : 1.f;
+  const float m = a.w ? (by_value ? s[1] : gt * s[1]) * a.inv_d * (rt * rt) : 0.f;
+  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
   if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
-    float v1[1] = {(sigmoid ? gt * (1.f - gt) : 1.f) * sr * s[2]};
+    float v1[1] = {(sigmoid ? gt * (1.f - gt) : 1.f) * rt * s[1]};
     store_v<1>(a.dgate, t * a.dgate_ld, a.gate_bf16, v1);
   }
   // dx in dres, the gate's gradient in g
-  MOE_EACH(c, k) {
-    const float x = q.x[c][k], av = q.g[c][k], sdy = sr * q.dy[c][k], da = sdy * av;
-    q.dres[c][k] = fmaf(da, st.w[c][k], fmaf(-m, x, q.dres[c][k]));
-    st.dw[c][k] = fmaf(da, x, st.dw[c][k]);
-    if (want_dg) {
-      const float gg = sdy * x * st.w[c][k] * (sigmoid ? av - av * av : 1.f);
+  if (by_value) {
+    MOE_EACH(c, k) {
+      const float x = q.x[c][k], av = q.g[c][k], da = __fmul_rn(q.dy[c][k], av);
+      q.dres[c][k] = __fadd_rn(q.dres[c][k], __fmul_rn(rt, fmaf(-x, m, __fmul_rn(da, st.w[c][k]))));
+      st.dw[c][k] = fmaf(da * rt, x, st.dw[c][k]);
+      const float gg = q.dy[c][k] * (x * rt * st.w[c][k]) * (sigmoid ? av * (1.f - av) : 1.f);
       st.dg[c][k] += gg;
       q.g[c][k] = gg;
+    }
+  } else {
+    MOE_EACH(c, k) {
+      const float x = q.x[c][k], da = __fmul_rn(q.dy[c][k], gt);
+      q.dres[c][k] = __fadd_rn(q.dres[c][k], __fmul_rn(rt, fmaf(-x, m, __fmul_rn(da, st.w[c][k]))));
+      st.dw[c][k] = fmaf(da * rt, x, st.dw[c][k]);
     }
   }
   store_row<V, NCH>(a.dx, t * a.dx_ld, a.dx_bf16, d, q.dres);
@@ -356,7 +374,7 @@ __device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, N
 // next row is loaded while this one is summed (without it, a row took 6 us of latency after latency:
 // 28 us for 4 rows a block).
 template <int V, int NCH>
-__global__ void __launch_bounds__(kNormMaxThreads) k_norm_bwd(const __grid_constant__ NormBwd a) {
+__global__ void __launch_bounds__(kNormMaxThreads, V * NCH <= 2 ? 3 : 0) k_norm_bwd(const __grid_constant__ NormBwd a) {
   constexpr bool NEXT = V * NCH <= 8;
   __shared__ __align__(16) float red[48];
   const int d = a.d, threads = blockDim.x;
