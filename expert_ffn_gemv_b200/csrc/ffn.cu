@@ -34,8 +34,6 @@ enum { kEpiPlain = 0, kEpiSwiglu = 1, kEpiDswiglu = 2 };
 struct GemmProb {
   int m, n, k, segs;       // segs products over k added up (operands a[i], b[i])
   int tiles_m, tiles_n;
-  int splits;              // the k range in so many pieces, piece s to out + s split_ld (fp32)
-  int64_t split_ld;
   int a[2], b[2];          // tensor map numbers
   int a_mn, b_mn;          // 1: the operand lies along its rows
   void *out;               // plain: [m][ld]
@@ -64,7 +62,7 @@ constexpr int kABytes = 128 * kBK * 2, kBBytes = 128 * kBK * 2, kStageBytes = kA
 constexpr int kGemmSmem = 1024 + 1024 + kStages * kStageBytes + kEpiWarps * 4096;
 
 struct GemmTile {
-  int p, m0, n0, s0, steps, split;  // k steps s0 .. s0 + steps - 1
+  int p, m0, n0, s0, steps;  // k steps s0 .. s0 + steps - 1
 };
 
 // The tiles of unit c of g (a unit: the CTAs of one tile): p[0]'s tiles c, c + g, ..; then the other
@@ -74,16 +72,16 @@ struct GemmTile {
 struct GemmWalk {
   int c, g, n0, rest, r, k0, i, phase;
   int cur;  // product whose numbers are held here: a tile is placed without loads or integer divisions
-  int tiles_m, tiles_n, steps, splits;
-  float inv_tiles, inv_band;
+  int tiles_m, tiles_n, steps;
+  float inv_band;
   __device__ GemmWalk(const GemmArgs &a, int c_, int g_) : c(c_), g(g_), i(0), phase(0), cur(-1) {
-    n0 = a.p[0].tiles_m * a.p[0].tiles_n * a.p[0].splits;
+    n0 = a.p[0].tiles_m * a.p[0].tiles_n;
     rest = 0;
     for (int p = 1; p < a.n_prob; ++p) rest += a.p[p].tiles_m * a.p[p].tiles_n;
     r = n0 % g;
     k0 = 0;
     if (rest) {
-      const int s0 = a.p[0].segs * a.p[0].k / a.p[0].splits, s1 = a.p[1].k;
+      const int s0 = a.p[0].segs * a.p[0].k, s1 = a.p[1].k;
       k0 = r ? (s0 + s1 / 2) / s1 : 0;
       if (static_cast<int64_t>(k0) * (g - r) > rest) k0 = rest / (g - r);
     }
@@ -129,15 +127,12 @@ struct GemmWalk {
     constexpr int kBand = 8;
     if (pi != cur) {
       const GemmProb &p = a.p[pi];
-      cur = pi, tiles_m = p.tiles_m, tiles_n = p.tiles_n, splits = p.splits;
+      cur = pi, tiles_m = p.tiles_m, tiles_n = p.tiles_n;
       steps = p.segs * ((p.k + kBK - 1) / kBK);
-      inv_tiles = 1.f / (tiles_m * tiles_n), inv_band = 1.f / (kBand * tiles_n);
+      inv_band = 1.f / (kBand * tiles_n);
     }
     t.p = pi;
-    t.split = splits > 1 ? div(j, tiles_m * tiles_n, inv_tiles) : 0;
-    j -= t.split * tiles_m * tiles_n;
-    t.s0 = splits > 1 ? steps * t.split / splits : 0;
-    t.steps = (splits > 1 ? steps * (t.split + 1) / splits : steps) - t.s0;
+    t.s0 = 0, t.steps = steps;
     const int band = div(j, kBand * tiles_n, inv_band), in = j - band * kBand * tiles_n;
     const int rows = min(kBand, tiles_m - band * kBand);
     t.n0 = rows == kBand ? in / kBand : in / rows;
@@ -288,7 +283,87 @@ __device__ __forceinline__ void store_f32(float *scratch, const uint32_t (&v)[32
   }
 }
 
-template <int EPI, int CG>
+// h and the gradients of g and u, where the gradient of h is dh
+__device__ __forceinline__ void dswiglu(float g, float u, float dh, float &h, float &dg, float &du) {
+  const float sg = sigmoid_f(g), sl = g * sg;
+  h = sl * u;
+  dg = dh * u * fmaf(sl, 1.f - sg, sg);
+  du = dh * sl;
+}
+
+// SPLIT: the k range of a tile is dealt to the CTAs of a cluster, which then lay their sums in shared
+// memory (the stages, no longer used), each as chunks of 32 x 32 values; every CTA adds up a share of the
+// values over the cluster, in the order of its CTAs, and finishes them.  For products with fewer tiles than
+// SMs: 64 tokens, d 4,096, f 768, forward 17 us, with the pieces of the down product alone split and added
+// up through global memory 33; 64 x 2,208 x 752, all gradients, 25 us (39).
+__device__ __forceinline__ int chunk_at(int row, int c4, int bn) {  // float4 c4 of a row, in 16-byte pieces
+  return ((row >> 5) * (bn >> 5) + (c4 >> 3)) * 256 + (row & 31) * 8 + ((c4 & 7) ^ (row & 7));
+}
+__device__ __forceinline__ float4 cluster_total(uint32_t base, int at, uint32_t ctas) {
+  float4 q[8];
+#pragma unroll
+  for (uint32_t r = 0; r < 8; ++r) {
+    if (r >= ctas) break;
+    uint32_t p;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(base + 16 * at), "r"(r));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(q[r].x), "=f"(q[r].y), "=f"(q[r].z), "=f"(q[r].w)
+                 : "r"(p)
+                 : "memory");
+  }
+  float4 d = q[0];
+#pragma unroll
+  for (uint32_t r = 1; r < 8; ++r)
+    if (r < ctas) d.x += q[r].x, d.y += q[r].y, d.z += q[r].z, d.w += q[r].w;
+  return d;
+}
+template <int EPI>
+__device__ __forceinline__ void split_epilogue(const GemmArgs &a, const GemmTile &tl, uint32_t base, uint32_t rank, uint32_t ctas,
+                                               int tid) {
+  const GemmProb &p = a.p[0];
+  const int wide = EPI == kEpiSwiglu ? a.bn / 2 : a.bn, log4 = 29 - __clz(wide);  // values of a row, log2 of its float4s
+  const int row0 = tl.m0 * 128, rows = min(128, p.m - row0), step = 32 * kEpiWarps;
+  for (int e = rank * step + tid; e < rows << log4; e += ctas * step) {
+    const int r = e >> log4, c4 = e & ((1 << log4) - 1), col = tl.n0 * wide + 4 * c4;
+    if (col >= p.n) continue;
+    const int64_t row = row0 + r;
+    const float4 q = cluster_total(base, chunk_at(r, c4, a.bn), ctas);
+    float d[4] = {q.x, q.y, q.z, q.w};
+    if (EPI == kEpiSwiglu) {
+      const float4 u = cluster_total(base, chunk_at(r, wide / 4 + c4, a.bn), ctas);
+      const int64_t at = row * a.f_ld + col;
+      if (a.g) {
+        *reinterpret_cast<float4 *>(a.g + at) = q;
+        *reinterpret_cast<float4 *>(a.u + at) = u;
+      }
+      const float w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = d[k] * sigmoid_f(d[k]) * w[k];
+      put4(a.h + at, d);
+    } else if (EPI == kEpiPlain) {
+      if (p.add) {
+        const float4 x = get4(p.add, row * p.add_ld + col, p.add_bf16);
+        d[0] += x.x, d[1] += x.y, d[2] += x.z, d[3] += x.w;
+      }
+      if (p.out_bf16)
+        put4(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld + col, d);
+      else
+        put4(static_cast<float *>(p.out) + row * p.ld + col, d);
+    } else {
+      const int64_t at = row * a.f_ld + col;
+      const float4 g = *reinterpret_cast<const float4 *>(a.g + at), u = *reinterpret_cast<const float4 *>(a.u + at);
+      const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+      float h[4], dg[4], du[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dswiglu(gv[k], uv[k], d[k], h[k], dg[k], du[k]);
+      put4(a.h + at, h);
+      put4(a.dg + at, dg);
+      put4(a.du + at, du);
+    }
+  }
+}
+
+template <int EPI, int CG, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_constant__ GemmArgs a) {
   constexpr int NS = kStages, EW = kEpiWarps;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -298,7 +373,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 516);
   unsigned char *stages = smem + 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / CG, units = gridDim.x / CG;
+  uint32_t part = 0, parts = 1;  // this CTA's piece of the k range
+  if (SPLIT) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+  }
+  const int size = SPLIT ? parts : CG, rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / size, units = gridDim.x / size;
   const int bn = a.bn, bl = bn / CG;  // columns of a tile, B rows of a CTA
   uint32_t *err = &g_ffn_err;
 
@@ -324,6 +404,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   griddep_launch();
   GemmWalk walk(a, unit, units);
   GemmTile tl;
+  auto next = [&]() {
+    if (!walk.next(a, tl)) return false;
+    if (SPLIT) {
+      tl.s0 = static_cast<int>(tl.steps * part / parts);
+      tl.steps = static_cast<int>(tl.steps * (part + 1) / parts) - tl.s0;
+    }
+    return true;
+  };
 
   if (warp == EW) {
     // ---------------- producer: this CTA's rows of both operands.  Lane l issues the step's copy l (the
@@ -332,7 +420,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
     uint32_t it = 0;
     bool ok = true;
     const uint32_t tx = CG * (kABytes + bl * kBK * 2);
-    while (ok && walk.next(a, tl)) {
+    while (ok && next()) {
       const GemmProb &p = a.p[tl.p];
       const int per = (p.k + kBK - 1) / kBK, m0 = (tl.m0 * CG + rank) * 128, na = p.a_mn ? 2 : 1;
       const bool is_a = lane < na, mine = lane < na + bl / 64, mn = is_a ? p.a_mn : p.b_mn;
@@ -377,7 +465,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
     if (lane == 0 && rank == 0) {
       uint32_t it = 0, n = 0;
       bool ok = true;
-      for (; ok && walk.next(a, tl); ++n) {
+      for (; ok && next(); ++n) {
         const GemmProb &p = a.p[tl.p];
         const int b = n & 1;
         if (n >= 2 && !(ok = pf_wait(&acc_empty[b], ((n >> 1) - 1) & 1u, kSpin, abort_flag, err))) break;
@@ -402,12 +490,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
       }
       if (it > 0) mbar_wait_bounded(&empty[(it - 1) % NS], ((it - 1) / NS) & 1u, kDrainLimit);
     }
+  } else if (SPLIT) {
+    // ---------------- epilogue, one tile: the sums to shared memory
+    const int c0 = 32 * (warp >> 2);
+    if (next() && __all_sync(0xffffffffu, pf_wait(&acc_full[0], 0u, kSpin, abort_flag, err)) && c0 < bn) {
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld32_nowait(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c0, v);
+      tmem_wait_ld();
+      turn_in(reinterpret_cast<float *>(stages) + ((warp & 3) * (bn / 32) + c0 / 32) * 1024, v, lane);
+    }
   } else {
     // ---------------- epilogue
     float *scratch = reinterpret_cast<float *>(stages + NS * kStageBytes + warp * 4096);
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     uint32_t n = 0;
-    while (walk.next(a, tl)) {
+    while (next()) {
       const int b = n & 1, rows = a.p[tl.p].m, cols = a.p[tl.p].n;
       const int row0 = (tl.m0 * CG + rank) * 128 + 32 * (warp & 3), first = 32 * (warp >> 2);
       const uint32_t acc = tmem + b * kMaxBN + quad;
@@ -470,7 +568,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
         void *out = a.p[tl.p].out;
         const int64_t ld = a.p[tl.p].ld, add_ld = a.p[tl.p].add_ld;
         const int out_bf16 = a.p[tl.p].out_bf16, add_bf16 = a.p[tl.p].add_bf16;
-        float *fout = static_cast<float *>(out) + tl.split * a.p[tl.p].split_ld;
         if (first >= bn) release();
         for (int c0 = first; c0 < bn; c0 += 8 * EW) {
           uint32_t v[32];
@@ -499,7 +596,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
             for (int i = 0; i < 16; ++i) h[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
             store_bf16(scratch, h, lane, static_cast<__nv_bfloat16 *>(out), ld, row0, rows, col, cols);
           } else {
-            store_f32(scratch, v, lane, fout, ld, row0, rows, col, cols);
+            store_f32(scratch, v, lane, static_cast<float *>(out), ld, row0, rows, col, cols);
           }
         }
       } else {
@@ -530,12 +627,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
               for (int k = 0; k < 4; ++k) {
                 float x[2][3];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float g = gv[2 * k + e], sg = sigmoid_f(g), sl = g * sg;
-                  x[e][0] = sl * uv[2 * k + e];
-                  x[e][1] = d[2 * k + e] * uv[2 * k + e] * fmaf(sl, 1.f - sg, sg);
-                  x[e][2] = d[2 * k + e] * sl;
-                }
+                for (int e = 0; e < 2; ++e) dswiglu(gv[2 * k + e], uv[2 * k + e], d[2 * k + e], x[e][0], x[e][1], x[e][2]);
                 hv[k] = pack2(x[0][0], x[1][0]), dg[k] = pack2(x[0][1], x[1][1]), du[k] = pack2(x[0][2], x[1][2]);
               }
               const int64_t at = row * a.f_ld + col;
@@ -549,41 +641,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
     }
   }
   __syncwarp();
+  if (SPLIT) {
+    cluster_sync();  // the sums of all CTAs are there
+    if (warp < EW) split_epilogue<EPI>(a, tl, smem_u32(stages), part, parts, tid);
+    __syncwarp();
+    cluster_sync();  // and have been read
+  }
   tc_fence_before();
   __syncthreads();
   // a CTA's shared memory is read by the pair's MMAs and its barriers are arrived on by the other CTA
   if (CG == 2) cluster_sync();
   if (warp == 0) g_tmem_dealloc<CG>(tmem);
-}
-
-// out = sum of the pieces of a split product, in order, (+ add)
-struct SumArgs {
-  const float *part;
-  const void *add;
-  void *out;
-  int64_t ld, add_ld, split_ld;
-  int m, n, splits, out_bf16, add_bf16;
-};
-__global__ void __launch_bounds__(256) k_ffn_sum(SumArgs a) {
-  griddep_wait();
-  griddep_launch();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= static_cast<int64_t>(a.m) * a.n) return;
-  const int64_t row = i / a.n, col = i - row * a.n;
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float4 q = *reinterpret_cast<const float4 *>(a.part + s * a.split_ld + i);
-    d[0] += q.x; d[1] += q.y; d[2] += q.z; d[3] += q.w;
-  }
-  if (a.add) {
-    const float4 e = get4(a.add, row * a.add_ld + col, a.add_bf16);
-    d[0] += e.x; d[1] += e.y; d[2] += e.z; d[3] += e.w;
-  }
-  if (a.out_bf16)
-    put4(static_cast<__nv_bfloat16 *>(a.out) + row * a.ld + col, d);
-  else
-    put4(static_cast<float *>(a.out) + row * a.ld + col, d);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -750,10 +818,12 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
 
 template <int EPI>
 cudaError_t configure_gemm() {
-  cudaError_t e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_ffn_gemm<EPI, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-  return e;
+  for (const void *k : {reinterpret_cast<const void *>(k_ffn_gemm<EPI, 1, false>), reinterpret_cast<const void *>(k_ffn_gemm<EPI, 2, false>),
+                        reinterpret_cast<const void *>(k_ffn_gemm<EPI, 1, true>)}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // Launch configuration: clusters of cg CTAs, programmatic stream serialization (the kernel may begin
@@ -777,9 +847,11 @@ struct Config {
   }
 };
 
+constexpr int kMaxParts = 8;
 struct FfnDevice {
   EncodeFn encode;
-  int nsm, pairs;  // CTA pairs the device holds at once
+  int nsm, pairs;              // CTA pairs the device holds at once
+  int clusters[kMaxParts + 1];  // and clusters of so many CTAs of a split product
 };
 
 // Once per device, with it current: the encoder's address, the kernels' shared-memory limit, sizes.
@@ -805,7 +877,11 @@ cudaError_t ffn_setup(FfnDevice *out) {
     if (e == cudaSuccess) e = configure_gemm<kEpiDswiglu>();
     if (e != cudaSuccess) return e;
     const Config two(2, kGemmThreads, kGemmSmem, 2, nullptr);
-    e = cudaOccupancyMaxActiveClusters(&k.pairs, k_ffn_gemm<kEpiPlain, 2>, &two.cfg);
+    e = cudaOccupancyMaxActiveClusters(&k.pairs, k_ffn_gemm<kEpiPlain, 2, false>, &two.cfg);
+    for (int c = 2; e == cudaSuccess && c <= kMaxParts; ++c) {
+      const Config of(c, kGemmThreads, kGemmSmem, c, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&k.clusters[c], k_ffn_gemm<kEpiPlain, 1, true>, &of.cfg);
+    }
     if (e != cudaSuccess) return e;
     if (k.pairs > k.nsm / 2) k.pairs = k.nsm / 2;
     k.encode = reinterpret_cast<EncodeFn>(fn);
@@ -836,38 +912,63 @@ struct Maps {
 
 GemmProb &add_prob(GemmArgs &a, int m, int n, int k) {
   GemmProb &p = a.p[a.n_prob++];
-  p.m = m, p.n = n, p.k = k, p.segs = p.splits = 1;
+  p.m = m, p.n = n, p.k = k, p.segs = 1;
   return p;
 }
 
-// Sizes the tiles and launches.  A unit is one CTA on tiles of 128 x bn or a pair of CTAs on tiles of
-// 256 x 256, which read half as many operand bytes for their products; the rule takes what fills the
-// device in the least time, by the clocks of a 64-deep step of each tile (kStep).
+// How a launch is tiled: a unit is one CTA on tiles of 128 x bn, a pair of CTAs on tiles of 256 x bn, which
+// read half as many operand bytes for their products, or (one product alone) a cluster of `parts` CTAs that
+// share the k range of a tile.  The rule takes what fills the device in the least time, by the clocks of a
+// 64-deep step of each tile.
+struct Form {
+  int cg, bn, step, parts;
+  double clocks;
+};
 template <int EPI>
-cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
-  struct Form {
-    int cg, bn, step;
-  };
-  constexpr Form forms[] = {{2, 256, 800}, {2, 128, 560}, {1, 128, 560}, {1, 64, 420}};
-  double best = 0;
-  Form f{};
-  for (const Form &c : forms) {
-    if (a.p[0].splits > 1 && (c.cg != 1 || c.bn != 128)) continue;
+Form choose_form(const GemmProb *prob, int n_prob, const FfnDevice &dev, bool split = true) {
+  constexpr struct { int cg, bn, step; } forms[] = {{2, 256, 800}, {2, 128, 560}, {1, 128, 560}, {1, 64, 420}};
+  constexpr int kFill = 4, kJoin = 4;  // steps' worth of filling and draining, of adding up over a cluster
+  Form best{};
+  for (const auto &c : forms) {
     if (EPI == kEpiSwiglu && c.bn == 64) continue;  // 64 rows each of two matrices at least
-    const int cols = EPI == kEpiSwiglu ? c.bn / 2 : c.bn, units = c.cg == 2 ? dev.pairs : dev.nsm;
-    if (units < 1) continue;
-    double steps = 0, longest = 0;  // of all tiles and of the longest
-    for (int i = 0; i < a.n_prob; ++i) {
-      const GemmProb &p = a.p[i];
-      const double len = p.segs * ((p.k + kBK - 1) / kBK) / p.splits + 4;  // 4: filling and draining
-      const double tiles = static_cast<double>((p.m + 128 * c.cg - 1) / (128 * c.cg)) * ((p.n + cols - 1) / cols) * p.splits;
-      // alone, whole rounds of tiles; among others, what is left over is filled up
-      steps += a.n_prob == 1 ? len * units * static_cast<int>((tiles + units - 1) / units) : len * tiles;
-      longest = longest > len ? longest : len;
+    const int cols = EPI == kEpiSwiglu ? c.bn / 2 : c.bn;
+    for (int parts = 1; parts <= (split && c.cg == 1 && n_prob == 1 ? kMaxParts : 1); ++parts) {
+      const int units = parts > 1 ? dev.clusters[parts] : c.cg == 2 ? dev.pairs : dev.nsm;
+      if (units < 1) continue;
+      double steps = 0, longest = 0;  // of all tiles and of the longest
+      bool fits = true;
+      for (int i = 0; i < n_prob; ++i) {
+        const GemmProb &p = prob[i];
+        const int deep = p.segs * ((p.k + kBK - 1) / kBK);
+        const double len = parts > 1 ? (deep + parts - 1) / parts + kFill + kJoin : deep + kFill;
+        const double tiles = static_cast<double>((p.m + 128 * c.cg - 1) / (128 * c.cg)) * ((p.n + cols - 1) / cols);
+        fits = fits && (parts == 1 || (deep >= parts && tiles * parts <= dev.nsm));
+        // alone, whole rounds of tiles; among others, what is left over is filled up
+        steps += n_prob == 1 ? len * units * static_cast<int>((tiles + units - 1) / units) : len * tiles;
+        longest = longest > len ? longest : len;
+      }
+      const double t = (steps / units > longest ? steps / units : longest) * c.step;
+      if (fits && (!best.cg || t < best.clocks)) best = Form{c.cg, c.bn, c.step, parts, t};
     }
-    const double t = (steps / units > longest ? steps / units : longest) * c.step;
-    if (!f.cg || t < best) best = t, f = c;
   }
+  return best;
+}
+
+// Whether dx is split over its k range in a launch of its own: where that takes less than its tiles beside
+// those of the weights' gradients.  By the sizes alone: dx has the same bits whatever else is asked for.
+bool dx_apart(int n, int d, int f, const FfnDevice &dev) {
+  constexpr double kLaunch = 4000;  // clocks
+  GemmProb p[4] = {};
+  p[0].m = n, p[0].n = d, p[0].k = f, p[0].segs = 2;
+  for (int i = 1; i < 4; ++i) p[i].m = i < 3 ? f : d, p[i].n = i < 3 ? d : f, p[i].k = n, p[i].segs = 1;
+  const Form alone = choose_form<kEpiPlain>(p, 1, dev), rest = choose_form<kEpiPlain>(p + 1, 3, dev);
+  // (a list of unlike tiles takes some 15 % longer than its sums say)
+  return alone.parts > 1 && alone.clocks + rest.clocks + kLaunch < 1.15 * choose_form<kEpiPlain>(p, 4, dev).clocks;
+}
+
+template <int EPI>
+cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st, bool split = true) {
+  const Form f = choose_form<EPI>(a.p, a.n_prob, dev, split);
   a.bn = f.bn;
   const int cols = EPI == kEpiSwiglu ? f.bn / 2 : f.bn;
   int tiles = 0;
@@ -875,11 +976,12 @@ cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st) {
     GemmProb &p = a.p[i];
     p.tiles_m = (p.m + 128 * f.cg - 1) / (128 * f.cg);
     p.tiles_n = (p.n + cols - 1) / cols;
-    tiles += p.tiles_m * p.tiles_n * p.splits;
+    tiles += p.tiles_m * p.tiles_n;
   }
-  const int units = f.cg == 2 ? dev.pairs : dev.nsm, grid = (tiles < units ? tiles : units) * f.cg;
-  const Config c(grid, kGemmThreads, kGemmSmem, f.cg, st);
-  return f.cg == 1 ? cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 1>, a) : cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 2>, a);
+  const int units = f.parts > 1 ? tiles : f.cg == 2 ? dev.pairs : dev.nsm, size = f.cg * f.parts;
+  const Config c((tiles < units ? tiles : units) * size, kGemmThreads, kGemmSmem, size, st);
+  if (f.parts > 1) return cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 1, true>, a);
+  return f.cg == 1 ? cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 1, false>, a) : cudaLaunchKernelEx(&c.cfg, k_ffn_gemm<EPI, 2, false>, a);
 }
 
 // Blocks of a cluster over k: enough clusters x blocks for four an SM, each of eight pieces of 64 at
@@ -907,44 +1009,12 @@ bool bad_shape(int n, int d, int f) {
 }
 uint64_t align_ws(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
-// Pieces of the k range (k values) of a product with n x d results: where these make fewer tiles of
-// 128 x 128 than a B200 has SMs, as many pieces as fill it, each of eight steps at least.  300 tokens,
-// d 2,048, f 8,192: the down product takes 49 us in one piece, its weights' bytes 5.
-int product_splits(int n, int d, int64_t k) {
-  const int64_t tiles = static_cast<int64_t>((n + 127) / 128) * ((d + 127) / 128), steps = (k + kBK - 1) / kBK;
-  int64_t s = tiles ? 148 / tiles : 1;
-  if (s > steps / 8) s = steps / 8;
-  return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
-}
-uint64_t split_bytes(int n, int d, int64_t k) {
-  const int s = product_splits(n, d, k);
-  return s > 1 ? align_ws(static_cast<uint64_t>(s) * n * d * 4) : 0;
-}
-
-// Sends a product's result through the pieces at `part` where it is split, and adds them up after the
-// launch.
-struct Split {
-  SumArgs sum{};
-  void set(GemmProb &q, float *part, int splits) {
-    q.splits = splits;
-    if (splits < 2) return;
-    sum = SumArgs{part, q.add, q.out, q.ld, q.add_ld, static_cast<int64_t>(q.m) * q.n, q.m, q.n, splits, q.out_bf16, q.add_bf16};
-    q.out = part, q.ld = q.n, q.out_bf16 = 0, q.add = nullptr, q.split_ld = sum.split_ld;
-  }
-  cudaError_t run(cudaStream_t st) const {
-    if (sum.splits < 2) return cudaSuccess;
-    const Config c(static_cast<int>((sum.split_ld / 4 + 255) / 256), 256, 0, 1, st);
-    return cudaLaunchKernelEx(&c.cfg, k_ffn_sum, sum);
-  }
-};
-
 }  // namespace
 
 extern "C" uint64_t moe_ffn_workspace(int32_t n_tokens, int32_t d_model, int32_t d_ff, int32_t backward) {
   if (bad_shape(n_tokens, d_model, d_ff)) return 0;
   const uint64_t nf = align_ws(static_cast<uint64_t>(n_tokens) * d_ff * 2);
-  if (backward) return 3 * nf + split_bytes(n_tokens, d_model, 2 * static_cast<int64_t>(d_ff));
-  return nf + (n_tokens > kSmallMax ? split_bytes(n_tokens, d_model, d_ff) : 0);
+  return backward ? 3 * nf : nf;
 }
 
 extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
@@ -991,7 +1061,6 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
   }
   if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
   GemmArgs b{};
-  Split split;
   {
     Maps m{dev.encode, b};
     GemmProb &q = add_prob(b, n, d, f);
@@ -999,11 +1068,9 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     q.b[0] = m.add(p->w_down, d, f, f, 64);
     q.out = p->y, q.ld = p->y_stride, q.out_bf16 = p->y_dtype == MOE_BF16;
     q.add = p->add, q.add_ld = p->add_stride, q.add_bf16 = p->add_dtype == MOE_BF16;
-    split.set(q, reinterpret_cast<float *>(h + align_ws(static_cast<uint64_t>(n) * f * 2) / 2), product_splits(n, d, f));
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
   e = launch_gemm<kEpiPlain>(b, dev, st);
-  if (e == cudaSuccess) e = split.run(st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1037,23 +1104,20 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
     if ((e = launch_gemm<kEpiDswiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
   }
-  // everything else in one launch: dx (its tiles run over both matrices), then the weights' gradients
+  // everything else in one launch: dx (its tiles run over both matrices), then the weights' gradients; few
+  // tokens: dx before them
   GemmArgs a{};
   Maps m{dev.encode, a};
-  Split split;
   if (p->dx) {
     GemmProb &q = add_prob(a, n, d, f);
     q.segs = 2;
     q.a[0] = m.add(dg, n, f, f, 128), q.a[1] = m.add(du, n, f, f, 128);
     q.b[0] = m.add(p->w_gate, f, d, d, kBK), q.b[1] = m.add(p->w_up, f, d, d, kBK), q.b_mn = 1;
     q.out = p->dx, q.ld = p->dx_stride, q.out_bf16 = 1;
-    split.set(q, reinterpret_cast<float *>(du + nf), product_splits(n, d, 2 * static_cast<int64_t>(f)));
-    // split, few tokens: the weights' gradients have other shapes of tiles, a launch of their own
-    if (q.splits > 1) {
+    const bool apart = dx_apart(n, d, f, dev);
+    if (apart || (!p->dw_gate && !p->dw_down)) {
       if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-      e = launch_gemm<kEpiPlain>(a, dev, st);
-      if (e == cudaSuccess) e = split.run(st);
-      if (e != cudaSuccess) return MOE_ERR_CUDA;
+      if (launch_gemm<kEpiPlain>(a, dev, st, apart) != cudaSuccess) return MOE_ERR_CUDA;
       a.n_prob = m.n = 0;
     }
   }
@@ -1072,7 +1136,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     q.out = p->dw_down, q.ld = f, q.out_bf16 = 1;
   }
   if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-  if (a.n_prob && (e = launch_gemm<kEpiPlain>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (a.n_prob && launch_gemm<kEpiPlain>(a, dev, st, false) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
