@@ -400,6 +400,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (warp == EW && lane < kMaxMaps)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.map[lane])) : "memory");
   griddep_wait();  // nothing above touched global memory
   griddep_launch();
   GemmWalk walk(a, unit, units);
