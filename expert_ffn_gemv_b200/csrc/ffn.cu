@@ -217,9 +217,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Fast division (2 ulp; 1 / inf = 0): the IEEE one made half of the epilogues' instructions.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -285,7 +282,7 @@ __device__ __forceinline__ void store_f32(float *scratch, const uint32_t (&v)[32
 
 // h and the gradients of g and u, where the gradient of h is dh
 __device__ __forceinline__ void dswiglu(float g, float u, float dh, float &h, float &dg, float &du) {
-  const float sg = sigmoid_f(g), sl = g * sg;
+  const float sg = fast_sigmoid(g), sl = g * sg;
   h = sl * u;
   dg = dh * u * fmaf(sl, 1.f - sg, sg);
   du = dh * sl;
@@ -338,7 +335,7 @@ __device__ __forceinline__ void split_epilogue(const GemmArgs &a, const GemmTile
       }
       const float w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) d[k] = d[k] * sigmoid_f(d[k]) * w[k];
+      for (int k = 0; k < 4; ++k) d[k] = d[k] * fast_sigmoid(d[k]) * w[k];
       put4(a.h + at, d);
     } else if (EPI == kEpiPlain) {
       if (p.add) {
@@ -559,7 +556,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
-            h[i] = pack2(g0 * sigmoid_f(g0) * __uint_as_float(w[2 * i]), g1 * sigmoid_f(g1) * __uint_as_float(w[2 * i + 1]));
+            h[i] = pack2(g0 * fast_sigmoid(g0) * __uint_as_float(w[2 * i]), g1 * fast_sigmoid(g1) * __uint_as_float(w[2 * i + 1]));
           }
           store_bf16(scratch, h, lane, a.h, a.f_ld, row0, rows, col, cols);
         } else {
@@ -775,7 +772,7 @@ __global__ void __launch_bounds__(kSmThreads, 8) k_ffn_up(SmallArgs a, int cl) {
     if (tok >= a.n) continue;
     const float gv = acc[e], uv = acc[2 + e];
     const int64_t at = static_cast<int64_t>(tok) * a.f + row;
-    a.h[at] = __float2bfloat16_rn(gv * sigmoid_f(gv) * uv);
+    a.h[at] = __float2bfloat16_rn(gv * fast_sigmoid(gv) * uv);
     if (a.g) {
       a.g[at] = gv;
       a.u[at] = uv;

@@ -178,22 +178,17 @@ __device__ __forceinline__ void clear_sums(float (&red)[N]) {
 }
 
 // a(g).  A gate of a row scales all its values, so that its last bit decides many roundings: it is taken
-// with expf and a division.  Gates by the value take the approximate forms, 3 units in the last place off
-// (8,192 x 4,096, a gate for every value: 55 us, 69 with the others).
+// with expf and a division.  Gates by the value take the fast form (8,192 x 4,096, a gate for every value:
+// 56 us, 69 with the other).
 __device__ __forceinline__ float gate_value(float g, int act) {
   return act == MOE_GATE_SIGMOID ? 1.0f / (1.0f + expf(-g)) : g;
-}
-__device__ __forceinline__ float gate_value_fast(float g) {
-  float r;  // (of infinity: 0)
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
-  return r;
 }
 // 1 / sqrt(sum / d + eps)
 __device__ __forceinline__ float root(float sum, float inv_d, float eps) { return rsqrtf(__fadd_rn(__fmul_rn(sum, inv_d), eps)); }
 
 template <int V, int NCH>
 __device__ __forceinline__ void gate_values(float (&g)[NCH][V], int act) {
-  if (act == MOE_GATE_SIGMOID) MOE_EACH(c, k) g[c][k] = gate_value_fast(g[c][k]);
+  if (act == MOE_GATE_SIGMOID) MOE_EACH(c, k) g[c][k] = fast_sigmoid(g[c][k]);
 }
 
 struct NormFwd {
