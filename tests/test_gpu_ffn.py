@@ -106,6 +106,48 @@ def test_long_products_of_few_tokens(P, n, d, f):
     assert torch.equal(P.ffn_backward(dy, x, *w, saved, need_dx=False)[3], got[3])
 
 
+@pytest.mark.parametrize("n", [9, 127, 129, 500])
+@pytest.mark.parametrize("d,f", [(4096, 776), (2056, 40), (72, 8192)])
+def test_narrow_blocks_and_models(P, n, d, f):
+    """Products with few tiles and long rows, in each of the three epilogues; rows behind the last stay."""
+    w = weights(d, f)
+    x, dy = randn(n, d, seed=5), randn(n, d, seed=6, std=0.1)
+    r = R.ffn(x, *w, dy)
+    rows = torch.full((n + 2, d), 7.0, device="cuda")
+    rows[:n] = randn(n, d, seed=7, dtype=F)
+    add = rows[:n].clone()
+    y, saved = P.ffn_forward(x, *w, add=rows[:n], out=rows[:n], save=True)
+    check_y(y, r, w[2], add)
+    assert (rows[n:] == 7.0).all()
+    for v, k, wt in zip(saved, ("g", "u"), w):
+        R.near(v, r[k], x.double().abs() @ wt.double().abs().T * 2.0 ** -13 + 1e-30, k)
+    got = P.ffn_backward(dy, x, *w, saved)
+    check_gradients(got, x, w, dy, r)
+    assert all(torch.equal(a, b) for a, b in zip(got, P.ffn_backward(dy, x, *w, saved)))
+    assert torch.equal(P.ffn_backward(dy, x, *w, saved, need_dw=False)[0], got[0])
+
+
+def test_two_streams_at_once(P):
+    """Calls of several shapes and forms beside one another: the bits of each alone."""
+    shapes = [(64, 1024, 512), (200, 512, 1024), (5, 1024, 1024), (700, 256, 768)]
+    data = [(randn(n, d, seed=i), randn(n, d, seed=i + 9, std=0.1), weights(d, f, seed=20 * i)) for i, (n, d, f) in enumerate(shapes)]
+
+    def step(x, dy, w):
+        y, saved = P.ffn_forward(x, *w, save=True)
+        return (y, *P.ffn_backward(dy, x, *w, saved))
+
+    want = [step(*v) for v in data]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, v in zip(streams, data):
+            with torch.cuda.stream(s):
+                got.append(step(*v))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, h in zip(got, want) for a, b in zip(g, h))
+
+
 def test_large(P):
     n, d, f = 2500, 2048, 2304
     w = weights(d, f)
