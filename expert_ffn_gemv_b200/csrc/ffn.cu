@@ -36,6 +36,7 @@ struct GemmProb {
   int tiles_m, tiles_n;
   int a[2], b[2];          // tensor map numbers
   int a_mn, b_mn;          // 1: the operand lies along its rows
+  int a_rows;              // K-major A: rows of a box, all that the one tile of up to 128 rows has, or 128
   void *out;               // plain: [m][ld]
   const void *add;         // plain: added to the result, or NULL
   int64_t ld, add_ld;
@@ -379,6 +380,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   const int bn = a.bn, bl = bn / CG;  // columns of a tile, B rows of a CTA
   uint32_t *err = &g_ffn_err;
 
+  if (warp == EW && lane < kMaxMaps)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.map[lane])) : "memory");
+  GemmWalk walk(a, unit, units);
+  GemmTile tl;
+  auto next = [&]() {
+    if (!walk.next(a, tl)) return false;
+    if (SPLIT) {
+      tl.s0 = static_cast<int>(tl.steps * part / parts);
+      tl.steps = static_cast<int>(tl.steps * (part + 1) / parts) - tl.s0;
+    }
+    return true;
+  };
+  bool have = next();  // the first tile is placed while the barriers and TMEM are set up
+
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -397,30 +412,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp == EW && lane < kMaxMaps)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.map[lane])) : "memory");
-  griddep_wait();  // nothing above touched global memory
-  griddep_launch();
-  GemmWalk walk(a, unit, units);
-  GemmTile tl;
-  auto next = [&]() {
-    if (!walk.next(a, tl)) return false;
-    if (SPLIT) {
-      tl.s0 = static_cast<int>(tl.steps * part / parts);
-      tl.steps = static_cast<int>(tl.steps * (part + 1) / parts) - tl.s0;
-    }
-    return true;
-  };
-
   if (warp == EW) {
     // ---------------- producer: this CTA's rows of both operands.  Lane l issues the step's copy l (the
     // one or two boxes of A, then those of B), with its map and coordinates worked out once a tile: one
     // lane that issued them all and looked them up spent 880 clocks a step on it, the MMAs take 512.
     uint32_t it = 0;
     bool ok = true;
-    const uint32_t tx = CG * (kABytes + bl * kBK * 2);
-    while (ok && next()) {
+    bool waited = false;
+    for (; ok && have; have = next()) {
       const GemmProb &p = a.p[tl.p];
+      const uint32_t tx = CG * ((p.a_mn ? kABytes : p.a_rows * kBK * 2) + bl * kBK * 2);
       const int per = (p.k + kBK - 1) / kBK, m0 = (tl.m0 * CG + rank) * 128, na = p.a_mn ? 2 : 1;
       const bool is_a = lane < na, mine = lane < na + bl / 64, mn = is_a ? p.a_mn : p.b_mn;
       const int box = is_a ? lane : lane - na;
@@ -438,6 +439,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
       const CUtensorMap *then = &a.map[m_then];
       if (tl.s0 > per) map = then;
       int k = (tl.s0 > per ? tl.s0 - per : tl.s0) * kBK;
+      if (!waited) {
+        griddep_wait();
+        griddep_launch();
+        waited = true;
+      }
       for (int s = tl.s0; s < tl.s0 + tl.steps; ++s, ++it) {
         const int st = it % NS;
         const bool got = it < NS || pf_wait(&empty[st], ((it / NS) - 1) & 1u, kSpin, abort_flag, err);
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
     if (lane == 0 && rank == 0) {
       uint32_t it = 0, n = 0;
       bool ok = true;
-      for (; ok && next(); ++n) {
+      for (; ok && have; have = next(), ++n) {
         const GemmProb &p = a.p[tl.p];
         const int b = n & 1;
         if (n >= 2 && !(ok = pf_wait(&acc_empty[b], ((n >> 1) - 1) & 1u, kSpin, abort_flag, err))) break;
@@ -492,7 +498,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   } else if (SPLIT) {
     // ---------------- epilogue, one tile: the sums to shared memory
     const int c0 = 32 * (warp >> 2);
-    if (next() && __all_sync(0xffffffffu, pf_wait(&acc_full[0], 0u, kSpin, abort_flag, err)) && c0 < bn) {
+    griddep_wait();
+    griddep_launch();
+    if (have && __all_sync(0xffffffffu, pf_wait(&acc_full[0], 0u, kSpin, abort_flag, err)) && c0 < bn) {
       tc_fence_after();
       uint32_t v[32];
       tmem_ld32_nowait(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c0, v);
@@ -504,7 +512,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
     float *scratch = reinterpret_cast<float *>(stages + NS * kStageBytes + warp * 4096);
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     uint32_t n = 0;
-    while (next()) {
+    griddep_wait();  // nothing before this touched global memory (nor do the MMA warp's lanes)
+    griddep_launch();
+    for (; have; have = next()) {
       const int b = n & 1, rows = a.p[tl.p].m, cols = a.p[tl.p].n;
       const int row0 = (tl.m0 * CG + rank) * 128 + 32 * (warp & 3), first = 32 * (warp >> 2);
       const uint32_t acc = tmem + b * kMaxBN + quad;
@@ -909,9 +919,10 @@ struct Maps {
   }
 };
 
+int box_rows(int m) { return m < 128 ? (m + 7) & ~7 : 128; }
 GemmProb &add_prob(GemmArgs &a, int m, int n, int k) {
   GemmProb &p = a.p[a.n_prob++];
-  p.m = m, p.n = n, p.k = k, p.segs = 1;
+  p.m = m, p.n = n, p.k = k, p.segs = 1, p.a_rows = box_rows(m);
   return p;
 }
 
@@ -1051,7 +1062,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
   {
     Maps m{dev.encode, a};
     GemmProb &q = add_prob(a, n, f, d);
-    q.a[0] = m.add(p->x, n, d, p->x_stride, 128);
+    q.a[0] = m.add(p->x, n, d, p->x_stride, box_rows(n));
     q.b[0] = m.add(p->w_gate, f, d, d, 64);
     q.b[1] = m.add(p->w_up, f, d, d, 64);
     a.h = h, a.g = static_cast<float *>(p->save_gate), a.u = static_cast<float *>(p->save_up);
@@ -1063,7 +1074,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
   {
     Maps m{dev.encode, b};
     GemmProb &q = add_prob(b, n, d, f);
-    q.a[0] = m.add(h, n, f, f, 128);
+    q.a[0] = m.add(h, n, f, f, box_rows(n));
     q.b[0] = m.add(p->w_down, d, f, f, 64);
     q.out = p->y, q.ld = p->y_stride, q.out_bf16 = p->y_dtype == MOE_BF16;
     q.add = p->add, q.add_ld = p->add_stride, q.add_bf16 = p->add_dtype == MOE_BF16;
@@ -1096,7 +1107,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     GemmArgs a{};
     Maps m{dev.encode, a};
     GemmProb &q = add_prob(a, n, f, d);
-    q.a[0] = m.add(p->dy, n, d, p->dy_stride, 128);
+    q.a[0] = m.add(p->dy, n, d, p->dy_stride, box_rows(n));
     q.b[0] = m.add(p->w_down, d, f, f, kBK), q.b_mn = 1;
     a.g = static_cast<float *>(const_cast<void *>(p->save_gate)), a.u = static_cast<float *>(const_cast<void *>(p->save_up));
     a.h = h, a.dg = dg, a.du = du, a.f_ld = f;
@@ -1110,7 +1121,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
   if (p->dx) {
     GemmProb &q = add_prob(a, n, d, f);
     q.segs = 2;
-    q.a[0] = m.add(dg, n, f, f, 128), q.a[1] = m.add(du, n, f, f, 128);
+    q.a[0] = m.add(dg, n, f, f, box_rows(n)), q.a[1] = m.add(du, n, f, f, box_rows(n));
     q.b[0] = m.add(p->w_gate, f, d, d, kBK), q.b[1] = m.add(p->w_up, f, d, d, kBK), q.b_mn = 1;
     q.out = p->dx, q.ld = p->dx_stride, q.out_bf16 = 1;
     const bool apart = dx_apart(n, d, f, dev);
