@@ -19,10 +19,9 @@
 // Precision: products of bf16 values with fp32 accumulators.  What is not bf16 by itself (fp32 x, and
 // v between the two products) enters as bf16 parts that add up to it: two where out is bf16 (2^-16 of
 // a value, far below the rounding of out), three where out is fp32 (exact).
+#include <cstdio>
 #include <mutex>
 #include <new>
-#include <string>
-#include <vector>
 
 #include "block.cuh"
 
@@ -647,32 +646,34 @@ class ErrorWords {
  public:
   uint32_t *take() {
     std::lock_guard<std::mutex> lock(mutex_);
-    if (free_.empty()) {
-      uint32_t *page = nullptr;
+    if (!free_) {
+      Word *page = nullptr;
       if (cudaHostAlloc(reinterpret_cast<void **>(&page), 4096, cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) {
         cudaGetLastError();
         return nullptr;
       }
-      for (int i = 0; i < 4096 / 64; ++i) free_.push_back(page + 16 * i);
+      for (size_t i = 0; i < 4096 / sizeof(Word); ++i) page[i].next = free_, free_ = page + i;
     }
-    uint32_t *w = free_.back();
-    free_.pop_back();
-    *w = 0;
-    return w;
+    Word *w = free_;
+    free_ = w->next;
+    w->err = 0;
+    return &w->err;
   }
-  void give(uint32_t *w) {
+  void give(uint32_t *err) {
     std::lock_guard<std::mutex> lock(mutex_);
-    free_.push_back(w);
+    Word *w = reinterpret_cast<Word *>(err);
+    w->next = free_, free_ = w;
   }
 
  private:
+  struct alignas(64) Word {
+    uint32_t err;
+    Word *next;  // of the words that no handle has
+  };
   std::mutex mutex_;
-  std::vector<uint32_t *> free_;
+  Word *free_ = nullptr;
 };
-ErrorWords &error_words() {
-  static ErrorWords *words = new ErrorWords;  // outlives every handle
-  return *words;
-}
+ErrorWords g_error_words;
 
 struct Device {
   int prev = -1;
@@ -698,7 +699,7 @@ struct moe_adapters {
   __nv_bfloat16 *a = nullptr, *b = nullptr, *stage = nullptr;
   AdMeta *meta = nullptr;
   uint32_t *err_host = nullptr, *err_dev = nullptr;
-  std::string last_error;
+  char last_error[160] = "";
 };
 
 namespace moe {
@@ -710,12 +711,12 @@ bool adapters_match(const moe_adapters *h, int d, int device, int n) {
 namespace {
 
 moe_status ad_fail(moe_adapters *h, moe_status s, const char *msg) {
-  h->last_error = msg;
+  snprintf(h->last_error, sizeof h->last_error, "%s", msg);
   return s;
 }
 moe_status ad_cuda(moe_adapters *h, cudaError_t e, const char *what) {
   cudaGetLastError();
-  h->last_error = std::string(what) + ": " + cudaGetErrorString(e);
+  snprintf(h->last_error, sizeof h->last_error, "%s: %s", what, cudaGetErrorString(e));
   return e == cudaErrorMemoryAllocation ? MOE_ERR_OUT_OF_MEMORY : MOE_ERR_CUDA;
 }
 
@@ -844,7 +845,7 @@ moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **ou
     e = cudaMemset(h->meta, 0, sizeof(AdMeta) * g.max_adapters);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) {
-      h->err_host = error_words().take();
+      h->err_host = g_error_words.take();
       e = h->err_host ? cudaHostGetDevicePointer(reinterpret_cast<void **>(&h->err_dev), h->err_host, 0) : cudaErrorMemoryAllocation;
     }
     if (e == cudaSuccess) e = current_sm_count(&h->nsm);
@@ -864,13 +865,13 @@ moe_status moe_adapters_destroy(moe_adapters *h) {
   Device dev(h->cfg.device);
   cudaDeviceSynchronize();
   if (h->mem) cudaFree(h->mem);
-  if (h->err_host) error_words().give(h->err_host);
+  if (h->err_host) g_error_words.give(h->err_host);
   cudaGetLastError();
   delete h;
   return MOE_OK;
 }
 
-const char *moe_adapters_last_error(const moe_adapters *h) { return h ? h->last_error.c_str() : "no handle"; }
+const char *moe_adapters_last_error(const moe_adapters *h) { return h ? h->last_error : "no handle"; }
 
 uint64_t moe_adapters_device_bytes(const moe_adapters *h) { return h ? h->bytes : 0; }
 
@@ -925,6 +926,8 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
     return ad_fail(h, MOE_ERR_INVALID_ARGUMENT, "a pointer or row stride is not a multiple of 16 bytes");
   if (n_tokens > 1 && (x_stride < g.d_in || base_stride < g.d_out || out_stride < g.d_out))
     return ad_fail(h, MOE_ERR_INVALID_ARGUMENT, "a row stride is smaller than a row");
+  if (base == out && n_tokens > 1 && base_stride != out_stride)
+    return ad_fail(h, MOE_ERR_INVALID_ARGUMENT, "out is base with another row stride");
   moe_status s = ad_pending(h);
   if (s != MOE_OK) return s;
   Device dev(g.device);
@@ -937,7 +940,7 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   a.x_ld = x_stride, a.base_ld = base_stride, a.out_ld = out_stride;
   a.n = n_tokens, a.d_in = g.d_in, a.d_out = g.d_out, a.slots = g.max_adapters, a.max_rank16 = h->r16;
   a.x_bf16 = x_dtype == MOE_BF16, a.io_bf16 = out_dtype == MOE_BF16;
-  a.in_place = base == out && base_stride == out_stride;
+  a.in_place = base == out;
   const int tm = tile_rows(n_tokens);
   const int64_t tiles = most_tiles(n_tokens, tm, g.max_adapters);
   cudaError_t e = cudaSuccess;

@@ -268,6 +268,9 @@ def test_refusals(P):
         with pytest.raises(P.MoeError) as e:
             h.apply(off, base, ids)
         assert e.value.status == P.MOE_ERR_INVALID_ARGUMENT and "16" in str(e.value)
+    both = torch.zeros(4, 128, dtype=BF, device="cuda")  # out is base with other rows than base's
+    assert P.lib().moe_adapters_apply(h.h, x.data_ptr(), P.MOE_BF16, 64, both.data_ptr(), 64, both.data_ptr(), 128, P.MOE_BF16,
+                                      ids.data_ptr(), 4, None) == P.MOE_ERR_INVALID_ARGUMENT
     many, mbase = data(17, 64, 64, BF, BF)
     with pytest.raises(P.MoeError):
         h.apply(many, mbase, torch.zeros(17, dtype=torch.int32, device="cuda"))
