@@ -32,6 +32,7 @@ namespace {
 constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;  // that compute; one more warp feeds them
 constexpr int kAdBlock = kAdThreads + 32;
 constexpr int kAdMaxRank = 128;
+constexpr int kSmSmem = 228 * 1024;  // of an SM, 1 KB of it taken by each block
 constexpr int kAdMaxTokens = 8192;
 constexpr int kAdMaxSlots = 4096;
 constexpr int kAdMaxD = 65536;
@@ -43,8 +44,7 @@ constexpr uint64_t kAdSpin = 2000000000ull;  // about a second
 // and at 64 (RC = 1).  In bytes they are what bounds long prompts: 64 KB an SM gave 3 TB/s.
 template <int XP, int VP, int RC>
 __host__ __device__ constexpr int ad_depth() { return XP == 1 && VP == 2 ? 4 : RC == 0 ? 4 : 3; }
-template <int TM, int XP, int VP, int RC>
-__host__ __device__ constexpr int ad_w_depth() { return TM != 64 ? 2 : RC == 0 || (XP == 1 && VP == 2) ? 4 : 2; }
+constexpr int kWDepth = 2;
 
 struct AdMeta {
   int rank;     // 0: slot not loaded
@@ -80,7 +80,7 @@ __host__ __device__ AdSmem ad_smem(int r16) {
   s.v = s.part + TM * r16 * 4;
   s.v_part = TM * s.v_ld * 2;
   s.w = (s.v + VP * s.v_part + 127) / 128 * 128;
-  s.total = s.w + kAdWarps / (TM / 16) * ad_w_depth<TM, XP, VP, RC>() * r16 * 64;
+  s.total = s.w + kAdWarps / (TM / 16) * kWDepth * r16 * 64;
   return s;
 }
 
@@ -463,7 +463,7 @@ template <int TM, int XP, int VP, int RC>
 __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__ AdArgs a) {
   constexpr int MG = TM / 16, KG = kAdWarps / MG;
   constexpr int XB = XP == 1 ? 2 : 4, IO = VP == 2 ? 2 : 4;  // bytes of a value of x; of base and out
-  constexpr int DW = ad_w_depth<TM, XP, VP, RC>();
+  constexpr int DW = kWDepth;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int rows[TM];
   const AdSmem S = ad_smem<TM, XP, VP, RC>(a.max_rank16);
@@ -726,7 +726,6 @@ moe_status ad_pending(moe_adapters *h) {
   return e ? ad_fail(h, MOE_ERR_DEVICE_FAULT, "an adapter id of an earlier call was out of range or not loaded") : MOE_OK;
 }
 
-int tile_rows(int n) { return n > 2048 ? 64 : n > 512 ? 32 : 16; }
 int64_t most_tiles(int n, int tm, int slots) { return n / tm + (n < slots + 1 ? n : slots + 1); }
 
 // Launch in clusters of cl blocks, with programmatic stream serialization (the kernels wait for the one
@@ -767,10 +766,8 @@ template <typename F>
 cudaError_t each_kernel(F f) {
   cudaError_t e = each_type<16, 0>(f);
   if (e == cudaSuccess) e = each_type<32, 0>(f);
-  if (e == cudaSuccess) e = each_type<64, 0>(f);
   if (e == cudaSuccess) e = each_type<16, 1>(f);
-  if (e == cudaSuccess) e = each_type<32, 1>(f);
-  return e == cudaSuccess ? each_type<64, 1>(f) : e;
+  return e == cudaSuccess ? each_type<32, 1>(f) : e;
 }
 
 // The kernels' shared-memory limit, once per device, with it current.
@@ -941,18 +938,23 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   a.n = n_tokens, a.d_in = g.d_in, a.d_out = g.d_out, a.slots = g.max_adapters, a.max_rank16 = h->r16;
   a.x_bf16 = x_dtype == MOE_BF16, a.io_bf16 = out_dtype == MOE_BF16;
   a.in_place = base == out;
-  const int tm = tile_rows(n_tokens);
-  const int64_t tiles = most_tiles(n_tokens, tm, g.max_adapters);
-  cudaError_t e = cudaSuccess;
-  int cl = 8;
-  while (cl > 1 && tiles * cl > 2 * h->nsm) cl >>= 1;
-  if (e == cudaSuccess)
-    e = each_kernel([&](auto tmc, auto xp, auto vp, auto rc) {
-      constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
-      if (TM != tm || (RC == 0) != (h->r16 <= 32) || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;
-      const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, ad_smem<TM, XP, VP, RC>(a.max_rank16).total, cl, st);
-      return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP, RC>, a);
-    });
+  const cudaError_t e = each_kernel([&](auto tmc, auto xp, auto vp, auto rc) {
+    constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
+    if ((RC == 0) != (h->r16 <= 32) || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;
+    // Tiles of 16 tokens, whose warps share k eight ways, where all of them fit on the device at once, else of
+    // 32, which read a group's weights half as often (2,048 -> 2,048, us, 16 and 32: 1,180 tokens of rank 16
+    // 13.0, 13.7; 4,096 of rank 64 25.6, 28.5; 8,192 58.9, 43.7; with tiles of 64: 48.9).
+    const auto room = [&](int smem) { return static_cast<int64_t>(h->nsm) * (2 * (smem + 1024) <= kSmSmem ? 2 : 1); };
+    const int small = ad_smem<16, XP, VP, RC>(a.max_rank16).total, smem = ad_smem<TM, XP, VP, RC>(a.max_rank16).total;
+    if (TM != (most_tiles(n_tokens, 16, g.max_adapters) <= room(small) ? 16 : 32)) return cudaSuccess;
+    // Blocks of a tile: as many as fit at once (clusters of two in two rounds took 28 us, single blocks in one
+    // 19: 1,180 tokens, 20 adapters of rank 64, fp32 x).
+    const int64_t tiles = most_tiles(n_tokens, TM, g.max_adapters), most = room(smem);
+    int cl = 8;
+    while (cl > 1 && tiles * cl > most) cl >>= 1;
+    const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, smem, cl, st);
+    return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP, RC>, a);
+  });
   return e == cudaSuccess ? MOE_OK : ad_cuda(h, e, "adapter launch");
 }
 
