@@ -726,6 +726,12 @@ moe_status ad_pending(moe_adapters *h) {
   return e ? ad_fail(h, MOE_ERR_DEVICE_FAULT, "an adapter id of an earlier call was out of range or not loaded") : MOE_OK;
 }
 
+// Clusters of a size that 148 SMs hold, at one block an SM.
+struct Cluster {
+  int size, held;
+};
+constexpr Cluster kClusters[] = {{8, 15}, {4, 33}, {3, 45}, {2, 74}};
+
 int64_t most_tiles(int n, int tm, int slots) { return n / tm + (n < slots + 1 ? n : slots + 1); }
 
 // Launch in clusters of cl blocks, with programmatic stream serialization (the kernels wait for the one
@@ -948,10 +954,11 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
     const int small = ad_smem<16, XP, VP, RC>(a.max_rank16).total, smem = ad_smem<TM, XP, VP, RC>(a.max_rank16).total;
     if (TM != (most_tiles(n_tokens, 16, g.max_adapters) <= room(small) ? 16 : 32)) return cudaSuccess;
     // Blocks of a tile: as many as fit at once (clusters of two in two rounds took 28 us, single blocks in one
-    // 19: 1,180 tokens, 20 adapters of rank 64, fp32 x).
+    // 19: 1,180 tokens, 20 adapters of rank 64, fp32 x; of three, 5 of rank 33, 19 us, of two 22).
     const int64_t tiles = most_tiles(n_tokens, TM, g.max_adapters), most = room(smem);
-    int cl = 8;
-    while (cl > 1 && tiles * cl > most) cl >>= 1;
+    int cl = 1;
+    for (const Cluster &c : kClusters)
+      if (cl == 1 && tiles * 148 <= most * c.held) cl = c.size;
     const AdConfig c(static_cast<int>(tiles) * cl, kAdBlock, smem, cl, st);
     return cudaLaunchKernelEx(&c.cfg, k_adapter<TM, XP, VP, RC>, a);
   });
