@@ -126,6 +126,21 @@ def test_many_slots_one_token_each(P):
     h.close()
 
 
+@pytest.mark.parametrize("xt,bt", [(BF, BF), (BF, F), (F, BF), (F, F)])
+@pytest.mark.parametrize("n,rank", [(127, 20), (128, 64), (129, 20), (129, 64), (4700, 16), (5001, 16), (8192, 32), (8191, 33)])
+def test_where_the_forms_change(P, n, rank, xt, bt):
+    """Both sides of the sizes at which ids are counted and tiles get wider; ids in any order."""
+    h, a, b, sc = make(P, 136, 72, [rank, 1, rank // 2], n, seed=4, slots=5)
+    ids = torch.randint(-1, 3, (n,), generator=rng(n)).to(torch.int32).cuda()
+    x, base = data(n, 136, 72, xt, bt)
+    out = h.apply(x, base, ids)
+    check(x, base, ids, a, b, sc, out, rank)
+    assert torch.equal(out, h.apply(x, base, ids)) and h.check() == P.MOE_OK
+    buf = base.clone()
+    assert torch.equal(h.apply(x, buf, ids, out=buf), out)
+    h.close()
+
+
 @pytest.mark.parametrize("host", [False, True])
 def test_replacing_and_emptying_a_slot(P, host):
     h, a, b, sc = make(P, 128, 64, [64, 8], 8, host=host)
