@@ -115,7 +115,7 @@ moe_block = _struct(
 EXPORTED = [
     "moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack", "moe_check", "moe_destroy",
     "moe_status_string", "moe_last_error", "moe_device_bytes", "moe_debug_set_spin_limit",
-    "moe_debug_set_alloc_cap", "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read",
+    "moe_debug_set_alloc_cap", "moe_debug_set_ring_spin_limit", "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read",
     "moe_route_noalloc",
     "moe_norm_in", "moe_norm_out", "moe_norm_workspace", "moe_norm_in_backward", "moe_norm_out_backward",
     "moe_adapters_create", "moe_adapters_load", "moe_adapters_apply", "moe_adapters_check", "moe_adapters_destroy",
@@ -153,6 +153,7 @@ def lib() -> C.CDLL:
         L.moe_device_bytes.restype = U64
         L.moe_debug_set_spin_limit.argtypes = [P, U64]
         L.moe_debug_set_alloc_cap.argtypes = [P, U64]
+        L.moe_debug_set_ring_spin_limit.argtypes = [U64]
         L.moe_debug_wait_test.argtypes = [P, P]
         L.moe_profile_enable.argtypes = [P, I]
         L.moe_profile_read.argtypes = [P, I, C.POINTER(C.c_float), C.POINTER(I)]
@@ -186,7 +187,7 @@ def lib() -> C.CDLL:
             getattr(L, name).restype = I
         for name in ("moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack", "moe_check",
                      "moe_destroy", "moe_debug_set_spin_limit", "moe_debug_set_alloc_cap",
-                     "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read", "moe_route_noalloc"):
+                     "moe_debug_set_ring_spin_limit", "moe_debug_wait_test", "moe_profile_enable", "moe_profile_read", "moe_route_noalloc"):
             getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -243,6 +244,10 @@ def moe_debug_set_spin_limit(h, cycles: int) -> int:
 
 def moe_debug_set_alloc_cap(h, nbytes: int) -> int:
     return lib().moe_debug_set_alloc_cap(h, nbytes)
+
+
+def moe_debug_set_ring_spin_limit(cycles: int) -> int:
+    return lib().moe_debug_set_ring_spin_limit(cycles)
 
 
 def moe_debug_wait_test(h, stream) -> int:

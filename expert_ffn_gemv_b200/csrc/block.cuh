@@ -14,6 +14,19 @@ bool adapters_match(const moe_adapters *h, int d, int device, int n);
 // Reads and clears the norms' error word on the current device (norms.cu).
 cudaError_t take_norm_error(uint32_t *err);
 
+// Clock cycles that a wait of a bulk-copy ring (norms.cu, adapters.cu) may take, and for which a ring's
+// first copies are held back (norms.cu): none, but where a test has the waits run out.
+struct RingSpin {
+  uint64_t limit, hold;
+};
+RingSpin ring_spin();
+
+__device__ __forceinline__ void hold_back(uint64_t clocks) {
+  const long long t0 = clock64();
+  while (static_cast<uint64_t>(clock64() - t0) < clocks) {
+  }
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SMs of the current device (asked once per device).

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, V * NCH <= 2 ? 3 : 0) k_norm_
 // never wait for a row's sums, and a row costs its arithmetic, not its latencies.
 // ------------------------------------------------------------------------------------------
 __device__ uint32_t g_norm_err;  // a bounded wait ran out
-constexpr uint64_t kNormSpin = 2000000000ull;
+constexpr uint64_t kRingSpin = 2000000000ull;  // about a second
+std::atomic<uint64_t> g_ring_limit{0};         // of a test, 0: the default
 constexpr int kRingMaxStages = 6, kRingMaxRows = 4;
 
 struct RowSource {
@@ -428,6 +429,7 @@ struct RowSource {
 struct Ring {
   RowSource src[kRingMaxRows];
   int n_src, stages, stage_bytes;
+  RingSpin spin;
 };
 
 struct RingState {
@@ -435,7 +437,7 @@ struct RingState {
   uint64_t *full, *empty;
   uint64_t limit;
   int threads;  // that compute: all warps but the last
-  __device__ RingState(unsigned char *smem, const Ring &r) : base(smem + 128), limit(kNormSpin), threads(blockDim.x - 32) {
+  __device__ RingState(unsigned char *smem, const Ring &r) : base(smem + 128), limit(r.spin.limit), threads(blockDim.x - 32) {
     full = reinterpret_cast<uint64_t *>(smem);
     empty = full + kRingMaxStages;
     if (threadIdx.x == 0) {
@@ -447,8 +449,9 @@ struct RingState {
     }
   }
   __device__ bool producer() const { return static_cast<int>(threadIdx.x) >= threads; }
-  // The last warp: lane i copies row i of a token, k-th token of this block after the other.  A wait
-  // that runs out ends it: the others then find no data, see wait().
+  // The last warp: lane i copies row i of a token, k-th token of this block after the other.  A stage is
+  // filled again when the others have given it back and the copies of its last fill have landed: the
+  // second follows from the first but where a wait of the others ran out.
   __device__ void produce(const Ring &r, int d, int n) const {
     const int lane = threadIdx.x & 31;
     const bool mine = lane < r.n_src;
@@ -459,19 +462,27 @@ struct RingState {
     const char *p = static_cast<const char *>(src.p) + blockIdx.x * src.ld * size;
     const int64_t step = static_cast<int64_t>(gridDim.x) * src.ld * size;
     int s = 0, phase = 1;
-    for (int64_t t = blockIdx.x; t < n; t += gridDim.x) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, kNormSpin))) {
+    uint32_t armed = 0;
+    for (int64_t t = blockIdx.x; t < n; t += gridDim.x, ++armed) {
+      const bool free = mbar_wait_bounded(&empty[s], phase, r.spin.limit);
+      const bool landed = armed < static_cast<uint32_t>(r.stages) || mbar_wait_bounded(&full[s], phase, kDrainLimit);
+      if (!__all_sync(0xffffffffu, free && landed)) {
         if (lane == 0) flag_error(&g_norm_err, kErrTimeout);
         break;
       }
       if (lane == 0) mbar_arrive_expect_tx(&full[s], r.stage_bytes);
+      if (armed == 0 && r.spin.hold) hold_back(r.spin.hold);
       __syncwarp();
       if (mine) bulk_g2s(base + s * r.stage_bytes + off, p, d * size, &full[s]);
       p += step;
       if (++s == r.stages) s = 0, phase ^= 1;
     }
-    // nothing may be on its way when the block leaves: the others have waited for every full stage, or
-    // given up; then wait here
+    // nothing may be on its way to the block's shared memory when it leaves: the last fill of every stage
+    // is waited for here, whatever the other warps did
+    __syncwarp();
+    if (lane == 0)
+      for (uint32_t k = armed > static_cast<uint32_t>(r.stages) ? armed - r.stages : 0; k < armed; ++k)
+        mbar_wait_bounded(&full[k % r.stages], (k / r.stages) & 1u, kDrainLimit);
     __syncwarp();
   }
   // A thread whose wait ran out sets the error word and does not wait again: what it then reads and
@@ -710,6 +721,7 @@ struct RingPlan {
     if (per_sm > n / (kRingRows * nsm)) per_sm = n / (kRingRows * nsm);
     int stages = (kRingBytes / per_sm - 1024) / r.stage_bytes;
     if (stages > kRingMaxStages) stages = kRingMaxStages;
+    r.spin = ring_spin();
     blocks = per_sm * nsm;
     smem = 128 + stages * r.stage_bytes;
     if (stages >= 2) r.stages = stages;
@@ -816,6 +828,11 @@ moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf
 using namespace moe;
 
 namespace moe {
+RingSpin ring_spin() {
+  const uint64_t v = g_ring_limit.load(std::memory_order_relaxed);
+  return v ? RingSpin{v, 4 * v} : RingSpin{kRingSpin, 0};
+}
+
 cudaError_t take_norm_error(uint32_t *err) {
   uint32_t v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_err, sizeof v);
@@ -825,6 +842,11 @@ cudaError_t take_norm_error(uint32_t *err) {
   return cudaMemcpyToSymbol(g_norm_err, &v, sizeof v);
 }
 }  // namespace moe
+
+extern "C" moe_status moe_debug_set_ring_spin_limit(uint64_t cycles) {
+  g_ring_limit.store(cycles, std::memory_order_relaxed);
+  return MOE_OK;
+}
 
 extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype,
                                   float eps, int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride,

@@ -1,0 +1,60 @@
+"""Waits of the block operators that run out: the call's status, and that nothing of it is left behind.
+
+A limit set by hand has the rings' first copies held back for longer than it, so that the waits for them run
+out.  The kernels then leave with an error word, once every copy of theirs has landed; the calls after them
+are right."""
+import pytest
+import torch
+
+import block_reference as R
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def P():
+    import expert_ffn_gemv_b200 as P
+
+    return P
+
+
+@pytest.fixture
+def limit(P):
+    """Sets the rings' limit, in clocks; the default comes back at the end."""
+    yield lambda clocks: P.moe_debug_set_ring_spin_limit(clocks)
+    P.moe_debug_set_ring_spin_limit(0)
+
+
+def randn(*shape, seed, std=1.0, mean=0.0, dtype=F):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std + mean).to(dtype)
+
+
+# sizes of every instantiation whose blocks are fed by a ring (at 2,048 columns from 1,776 rows on)
+@pytest.mark.parametrize("n,d,back", [(2000, 264, False), (2000, 264, True), (1900, 2048, False), (1900, 2048, True),
+                                      (2500, 4096, False), (2500, 4096, True), (700, 8192, False)])
+@pytest.mark.parametrize("clocks", [20_000, 2_000_000])  # 10 us, 1 ms
+def test_norm_rings(P, limit, n, d, back, clocks):
+    o, res, w = randn(n, d, seed=1, std=0.5, dtype=BF), randn(n, d, seed=2), randn(d, seed=3, std=0.3, mean=1.0)
+
+    def call():
+        if back:
+            return P.norm_out_backward(o, res, weight=w, eps=R.EPS)[:2]
+        return P.norm_out(o, res, weight=w, eps=R.EPS, next_weight=w, next_eps=R.EPS)
+
+    want = call()
+    assert P.block_check() == P.MOE_OK
+    limit(clocks)
+    for _ in range(3):
+        got = call()
+        torch.cuda.synchronize()
+        status = P.block_check()
+        # (a hardware wait may suspend a thread for longer than the shorter limit)
+        assert status == P.MOE_ERR_TIMEOUT or (clocks < 2_000_000 and all(torch.equal(a, b) for a, b in zip(got, want)))
+        assert P.block_check() == P.MOE_OK  # reported once
+    limit(0)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    assert P.block_check() == P.MOE_OK
