@@ -41,7 +41,6 @@ constexpr int kAdMaxD = 65536;
 constexpr int kAdInKernel = 128;
 constexpr int kAdGroups = 8;        // n8 rank groups of one pass over x: 64 ranks
 constexpr int kRedLd = 8 * kAdGroups + 8;
-constexpr uint64_t kAdSpin = 2000000000ull;  // about a second
 // Pieces of x and base, and of weights, on their way: what fits two blocks on an SM at 32 ranks (RC = 0)
 // and at 64 (RC = 1).  In bytes they are what bounds long prompts: 64 KB an SM gave 3 TB/s.
 template <int XP, int VP, int RC>
@@ -63,6 +62,7 @@ struct AdArgs {
   int64_t x_ld, base_ld, out_ld, a_slot, b_slot;
   int n, d_in, d_out, slots, max_rank16;
   int x_bf16, io_bf16, in_place;
+  RingSpin spin;
 };
 
 __host__ __device__ constexpr int round16(int r) { return (r + 15) & ~15; }
@@ -321,15 +321,21 @@ struct AdRing {
   __device__ __forceinline__ void next() {
     if (++stage == DEPTH) stage = 0, phase ^= 1;
   }
-  // feeding lane: a piece of n bytes, when the stage is free
-  __device__ __forceinline__ bool put(const void *src, int n) {
-    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, kAdSpin)) return false;
+  // feeding lane: a piece of n bytes, when the stage is free and the copy of its last fill has landed (the
+  // second follows from the first but where a wait of the warps ran out)
+  __device__ __forceinline__ bool put(const void *src, int n, uint64_t limit) {
+    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, limit) || !mbar_wait_bounded(&full[stage], phase ^ 1, kDrainLimit))
+      return false;
     mbar_arrive_expect_tx(&full[stage], n);
     bulk_g2s(base + stage * bytes, src, n, &full[stage]);
     next();
     return true;
   }
-  // A warp whose wait ran out sets the error word and does not wait again: what it then multiplies is
+  // feeding lane, at its end: nothing may be on its way to the block's shared memory when it leaves
+  __device__ __forceinline__ void drain() const {
+    for (int s = 0; s < DEPTH; ++s) mbar_wait_bounded(&full[s], s < stage ? phase : phase ^ 1, kDrainLimit);
+  }
+  // A thread whose wait ran out sets the error word and does not wait again: what it then multiplies is
   // in bounds, and every barrier is still reached.
   __device__ __forceinline__ uint32_t take(uint64_t &limit, uint32_t *err) const {
     if (!mbar_wait_bounded(&full[stage], phase, limit)) {
@@ -504,28 +510,30 @@ __global__ void __launch_bounds__(kAdBlock, 2) k_adapter(const __grid_constant__
     const bool mine = lane < KG;
     AdRing<DW> ring(smem, S, a.max_rank16, mine ? lane : 0, KG);
     bool ok = mine;
+    if (a.spin.hold) hold_back(a.spin.hold);
     const __nv_bfloat16 *ap = a.a + a.a_slot * adapter, *bp = a.b + a.b_slot * adapter;
     for (int g0 = 0; g0 < ng; g0 += kAdGroups) {
       const int nj = min(kAdGroups, ng - g0);
-      for (int kb = kb0 + lane; kb < kb1 && ok; kb += KG) ok = ring.put(ap + (static_cast<int64_t>(kb) * ng + g0) * 256, nj * 512);
+      for (int kb = kb0 + lane; kb < kb1 && ok; kb += KG) ok = ring.put(ap + (static_cast<int64_t>(kb) * ng + g0) * 256, nj * 512, a.spin.limit);
     }
     // the first pieces of the second product, then the block's part in the cluster's barriers
     int nb = nb0 + lane, first = 0;
-    for (; nk && nb < nb1 && first < DW && ok; nb += KG, ++first) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024);
+    for (; nk && nb < nb1 && first < DW && ok; nb += KG, ++first) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024, a.spin.limit);
     __syncwarp();
     if (cl > 1) {
       cluster_arrive();
       cluster_wait();
       cluster_arrive();
     }
-    for (; nk && nb < nb1 && ok; nb += KG) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024);
+    for (; nk && nb < nb1 && ok; nb += KG) ok = ring.put(bp + static_cast<int64_t>(nb) * nk * 512, nk * 1024, a.spin.limit);
     if (mine && !ok) flag_error(a.err, kErrTimeout);
+    if (mine) ring.drain();
     __syncwarp();
     if (cl > 1) cluster_wait();
     return;
   }
 
-  uint64_t limit = kAdSpin;
+  uint64_t limit = a.spin.limit;
   AdRing<DW> ring(smem, S, a.max_rank16, kg, KG);
   AdLane l;
   l.lane = tid & 31, l.q = tid & 3, l.slot = smem_u32(smem + S.ring) + tid * 16;
@@ -946,6 +954,7 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   a.n = n_tokens, a.d_in = g.d_in, a.d_out = g.d_out, a.slots = g.max_adapters, a.max_rank16 = h->r16;
   a.x_bf16 = x_dtype == MOE_BF16, a.io_bf16 = out_dtype == MOE_BF16;
   a.in_place = base == out;
+  a.spin = ring_spin();
   const cudaError_t e = each_kernel([&](auto tmc, auto xp, auto vp, auto rc) {
     constexpr int TM = decltype(tmc)::value, XP = decltype(xp)::value, VP = decltype(vp)::value, RC = decltype(rc)::value;
     if ((RC == 0) != (h->r16 <= 32) || (VP == 2) != (a.io_bf16 != 0) || (XP == 1) != (a.x_bf16 != 0)) return cudaSuccess;

@@ -374,8 +374,8 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
 /* Test hooks.  moe_debug_set_spin_limit: clock cycles a device-side bounded wait may spin
  * before it gives up (0 restores the default of about one second).  moe_debug_set_alloc_cap:
  * fail allocations that would take the handle above `bytes` (0 = no cap).
- * moe_debug_set_ring_spin_limit: the same limit for the bulk-copy rings of the norms over many rows,
- * process-wide, for the launches that follow; each block's first copies are then held back for four
+ * moe_debug_set_ring_spin_limit: the same limit for the bulk-copy rings of the norms over many rows
+ * and of the adapters, process-wide, for the launches that follow; each block's first copies are then held back for four
  * times as long, so that the waits for them run out. */
 moe_status moe_debug_set_spin_limit(moe_handle *h, uint64_t cycles);
 moe_status moe_debug_set_alloc_cap(moe_handle *h, uint64_t bytes);

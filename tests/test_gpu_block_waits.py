@@ -58,3 +58,31 @@ def test_norm_rings(P, limit, n, d, back, clocks):
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
     assert P.block_check() == P.MOE_OK
+
+
+@pytest.mark.parametrize("xt,bt", [(BF, BF), (BF, F), (F, BF), (F, F)])
+@pytest.mark.parametrize("n,rank", [(5, 16), (300, 33), (2500, 128)])  # clusters, single blocks, both tile sizes
+@pytest.mark.parametrize("clocks", [20_000, 2_000_000])
+def test_adapter_rings(P, limit, n, rank, xt, bt, clocks):
+    h = P.Adapters(d_in=520, d_out=1032, max_adapters=2, max_rank=rank, max_tokens=n)
+    for i in range(2):
+        h.load(i, randn(rank - i, 520, seed=i, std=0.05, dtype=BF), randn(1032, rank - i, seed=5 + i, std=0.2, dtype=BF), 0.5 + i)
+    x, base = randn(n, 520, seed=7, dtype=xt), randn(n, 1032, seed=8, dtype=bt)
+    ids = (torch.arange(n) % 3 - 1).to(torch.int32).cuda()
+    want = h.apply(x, base, ids)
+    torch.cuda.synchronize()
+    assert h.check() == P.MOE_OK
+    limit(clocks)
+    for _ in range(3):
+        got = h.apply(x, base, ids)
+        torch.cuda.synchronize()
+        status = h.check()
+        assert status == P.MOE_ERR_TIMEOUT or (clocks < 2_000_000 and torch.equal(got, want))
+        assert torch.equal(got[ids == -1], base[ids == -1])  # these wait for nothing
+        assert h.check() == P.MOE_OK
+    limit(0)
+    for _ in range(3):
+        assert torch.equal(h.apply(x, base, ids), want)
+    torch.cuda.synchronize()
+    assert h.check() == P.MOE_OK
+    h.close()
