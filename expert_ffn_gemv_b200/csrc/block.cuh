@@ -11,8 +11,13 @@ namespace moe {
 // Whether the handle adapts d -> d on this device and takes n tokens a call (adapters.cu).
 bool adapters_match(const moe_adapters *h, int d, int device, int n);
 
-// Reads and clears the norms' error word on the current device (norms.cu).
-cudaError_t take_norm_error(uint32_t *err);
+// The current device's error word of the norms and the dense block: host memory that kernels write, so
+// that the host can read and clear it in one step (norms.cu).  A first use allocates the words of all
+// devices, also while a stream is captured.
+struct BlockWord {
+  uint32_t *host = nullptr, *dev = nullptr;
+};
+cudaError_t block_word(BlockWord *w);
 
 // Clock cycles that a wait of a bulk-copy ring (norms.cu, adapters.cu) may take, and for which a ring's
 // first copies are held back (norms.cu): none, but where a test has the waits run out.

@@ -26,9 +26,6 @@ constexpr int kMaxBN = 256;
 constexpr uint64_t kSpin = 2000000000ull;  // about a second
 constexpr int kMaxProb = 4, kMaxMaps = 9;
 
-// Set by a kernel whose bounded wait ran out; moe_block_check reads and clears it.
-__device__ uint32_t g_ffn_err;
-
 enum { kEpiPlain = 0, kEpiSwiglu = 1, kEpiDswiglu = 2 };
 
 struct GemmProb {
@@ -47,6 +44,7 @@ struct GemmArgs {
   CUtensorMap map[kMaxMaps];
   GemmProb p[kMaxProb];    // p[0] is dealt out first, then the others as one list
   int n_prob, bn;          // bn: columns of a tile (swiglu: bn / 2 of g and of u)
+  uint32_t *err;           // set where a bounded wait ran out
   // gated epilogues: n columns of f values
   float *g, *u;                // swiglu: saved unless NULL; dswiglu: read
   __nv_bfloat16 *h, *dg, *du;  // swiglu: h; dswiglu: all three
@@ -381,7 +379,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_ffn_gemm(const __grid_const
   }
   const int size = SPLIT ? parts : CG, rank = CG == 2 ? blockIdx.x & 1 : 0, unit = blockIdx.x / size, units = gridDim.x / size;
   const int bn = a.bn, bl = bn / CG;  // columns of a tile, B rows of a CTA
-  uint32_t *err = &g_ffn_err;
+  uint32_t *err = a.err;
 
   if (warp == EW && lane < kMaxMaps)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.map[lane])) : "memory");
@@ -983,6 +981,10 @@ template <int EPI>
 cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st, bool split = true) {
   const Form f = choose_form<EPI>(a.p, a.n_prob, dev, split);
   a.bn = f.bn;
+  BlockWord word;
+  const cudaError_t e = block_word(&word);
+  if (e != cudaSuccess) return e;
+  a.err = word.dev;
   const int cols = EPI == kEpiSwiglu ? f.bn / 2 : f.bn;
   int tiles = 0;
   for (int i = 0; i < a.n_prob; ++i) {
@@ -1154,16 +1156,12 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
 }
 
 extern "C" moe_status moe_block_check(void) {
-  uint32_t v = 0, w = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_ffn_err, sizeof v);
-  if (e == cudaSuccess) e = take_norm_error(&w);
-  if (e == cudaSuccess && v) {
-    const uint32_t zero = 0;
-    e = cudaMemcpyToSymbol(g_ffn_err, &zero, sizeof zero);
-  }
+  BlockWord w;
+  cudaError_t e = cudaDeviceSynchronize();  // every stream of the device, also those that no other waits for
+  if (e == cudaSuccess) e = block_word(&w);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  return v || w ? MOE_ERR_TIMEOUT : MOE_OK;
+  return __atomic_exchange_n(w.host, 0u, __ATOMIC_ACQ_REL) ? MOE_ERR_TIMEOUT : MOE_OK;
 }

@@ -18,8 +18,10 @@
 // device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No atomics:
 // the same call gives the same bits.
 #include <math.h>
+#include <string.h>
 
 #include <initializer_list>
+#include <mutex>
 
 #include "block.cuh"
 
@@ -416,7 +418,6 @@ __global__ void __launch_bounds__(kNormMaxThreads, V * NCH <= 2 ? 3 : 0) k_norm_
 // warp refills a stage when the others have its values in registers, so the copies of the next rows
 // never wait for a row's sums, and a row costs its arithmetic, not its latencies.
 // ------------------------------------------------------------------------------------------
-__device__ uint32_t g_norm_err;  // a bounded wait ran out
 constexpr uint64_t kRingSpin = 2000000000ull;  // about a second
 std::atomic<uint64_t> g_ring_limit{0};         // of a test, 0: the default
 constexpr int kRingMaxStages = 6, kRingMaxRows = 4;
@@ -430,6 +431,7 @@ struct Ring {
   RowSource src[kRingMaxRows];
   int n_src, stages, stage_bytes;
   RingSpin spin;
+  uint32_t *err;  // set where a bounded wait ran out
 };
 
 struct RingState {
@@ -467,7 +469,7 @@ struct RingState {
       const bool free = mbar_wait_bounded(&empty[s], phase, r.spin.limit);
       const bool landed = armed < static_cast<uint32_t>(r.stages) || mbar_wait_bounded(&full[s], phase, kDrainLimit);
       if (!__all_sync(0xffffffffu, free && landed)) {
-        if (lane == 0) flag_error(&g_norm_err, kErrTimeout);
+        if (lane == 0) flag_error(r.err, kErrTimeout);
         break;
       }
       if (lane == 0) mbar_arrive_expect_tx(&full[s], r.stage_bytes);
@@ -490,7 +492,7 @@ struct RingState {
   __device__ __forceinline__ const unsigned char *wait(const Ring &r, int s, int phase) {
     if (!mbar_wait_bounded(&full[s], phase, limit)) {
       limit = 0;
-      flag_error(&g_norm_err, kErrTimeout);
+      flag_error(r.err, kErrTimeout);
     }
     return base + s * r.stage_bytes;
   }
@@ -722,6 +724,9 @@ struct RingPlan {
     int stages = (kRingBytes / per_sm - 1024) / r.stage_bytes;
     if (stages > kRingMaxStages) stages = kRingMaxStages;
     r.spin = ring_spin();
+    BlockWord word;
+    if ((err = block_word(&word)) != cudaSuccess) return;
+    r.err = word.dev;
     blocks = per_sm * nsm;
     smem = 128 + stages * r.stage_bytes;
     if (stages >= 2) r.stages = stages;
@@ -833,13 +838,34 @@ RingSpin ring_spin() {
   return v ? RingSpin{v, 4 * v} : RingSpin{kRingSpin, 0};
 }
 
-cudaError_t take_norm_error(uint32_t *err) {
-  uint32_t v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_err, sizeof v);
-  *err = v;
-  if (e != cudaSuccess || !v) return e;
-  v = 0;
-  return cudaMemcpyToSymbol(g_norm_err, &v, sizeof v);
+cudaError_t block_word(BlockWord *w) {
+  constexpr int kMaxDevices = 64, kWordBytes = 64;
+  static std::mutex mutex;
+  static char *page = nullptr;
+  static std::atomic<char *> known[kMaxDevices];  // the page as the device sees it
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorNotSupported;
+  char *seen = known[dev].load(std::memory_order_acquire);
+  if (!seen) {
+    std::lock_guard<std::mutex> lock(mutex);
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // this allocation is no part of any capture
+    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+    if (!page) {
+      void *p = nullptr;
+      e = cudaHostAlloc(&p, kMaxDevices * kWordBytes, cudaHostAllocMapped | cudaHostAllocPortable);
+      if (e == cudaSuccess) page = static_cast<char *>(memset(p, 0, kMaxDevices * kWordBytes));
+    }
+    void *p = nullptr;
+    if (e == cudaSuccess) e = cudaHostGetDevicePointer(&p, page, 0);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    known[dev].store(seen = static_cast<char *>(p), std::memory_order_release);
+  }
+  w->host = reinterpret_cast<uint32_t *>(page + dev * kWordBytes);
+  w->dev = reinterpret_cast<uint32_t *>(seen + dev * kWordBytes);
+  return cudaSuccess;
 }
 }  // namespace moe
 

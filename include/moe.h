@@ -196,12 +196,15 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * layer, so a quantised layer can be tuned against its original with the routed experts frozen).
  * All of them take device pointers, run on the current device (adapters: on their handle's),
  * enqueue on `stream`, never synchronise the host and allocate nothing, so they can be captured
- * into a CUDA graph (after a first call outside a capture, which loads and configures kernels).  Strides count values between the starts of consecutive rows.  Each result is
+ * into a CUDA graph (after a first call outside a capture, which loads and configures kernels and
+ * pins a page of host memory for error words).  Strides count values between the starts of
+ * consecutive rows.  Each result is
  * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
  * Outputs may not overlap inputs unless said so.
  * ------------------------------------------------------------------------------------------- */
-/* Waits for the current device and returns (and clears) a pending MOE_ERR_TIMEOUT of the norms' and
- * the dense block's kernels there: a bounded wait ran out and the results of a call are not valid. */
+/* Waits for the current device, all its streams, and returns (and clears) a pending MOE_ERR_TIMEOUT of
+ * the norms' and the dense block's kernels there, whoever called them: a bounded wait ran out and the
+ * results of a call are not valid. */
 moe_status moe_block_check(void);
 
 /* What a gate is broadcast over: one value per column, per token, or of its own for every value. */

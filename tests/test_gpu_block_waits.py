@@ -86,3 +86,19 @@ def test_adapter_rings(P, limit, n, rank, xt, bt, clocks):
     torch.cuda.synchronize()
     assert h.check() == P.MOE_OK
     h.close()
+
+
+def test_check_waits_for_every_stream(P, limit):
+    """torch's streams wait for nobody: the check has to."""
+    x, w = randn(2000, 1024, seed=1), randn(1024, seed=2)
+    side = torch.cuda.Stream()
+    P.norm_in(x, w)
+    for clocks, status in ((0, P.MOE_OK), (2_000_000, P.MOE_ERR_TIMEOUT), (0, P.MOE_OK)):
+        limit(clocks)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # 50 ms
+            P.norm_in(x, w)
+        assert not side.query()
+        assert P.block_check() == status
+        assert side.query()
