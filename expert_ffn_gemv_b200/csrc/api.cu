@@ -725,8 +725,8 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
   // the block input a and the block output o (fp32) take the staging buffers, x the residual buffer
   void *a = h->x_stage;
   float *o = static_cast<float *>(h->y_stage), *res = h->res[0];
-  s = moe_norm_in(x_in, g.act_dtype, D, blocks[0].norm_in_w, blocks[0].norm_dtype, blocks[0].norm_in_eps,
-                  blocks[0].unit_offset, a, g.act_dtype, D, n_tokens, D, stream);
+  s = norm_in_run(x_in, g.act_dtype, D, blocks[0].norm_in_w, blocks[0].norm_dtype, blocks[0].norm_in_eps,
+                  blocks[0].unit_offset, a, g.act_dtype, D, n_tokens, D, stream, h->err_dev);
   if (s != MOE_OK) return fail(h, s, "input norm");
   for (int i = 0; i < n_layers; ++i) {
     const moe_block &b = blocks[i];
@@ -743,7 +743,7 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
       f.add = o, f.add_dtype = MOE_F32, f.add_stride = D;
       f.y = o, f.y_dtype = MOE_F32, f.y_stride = D;
       f.workspace = workspace, f.workspace_bytes = workspace_bytes;
-      if ((s = moe_ffn_forward(&f, stream)) != MOE_OK) return fail(h, s, "dense block");
+      if ((s = ffn_forward_run(&f, stream, h->err_dev)) != MOE_OK) return fail(h, s, "dense block");
     }
     if (b.adapters) {
       s = moe_adapters_apply(b.adapters, a, g.act_dtype, D, o, D, o, D, MOE_F32, adapter_ids, n_tokens, stream);
@@ -764,11 +764,11 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
       q.next_weight = blocks[i + 1].norm_in_w, q.next_eps = blocks[i + 1].norm_in_eps;
       q.h = a, q.h_dtype = g.act_dtype, q.h_stride = D;
     }
-    if ((s = moe_norm_out(&q, stream)) != MOE_OK) return fail(h, s, "output norm");
+    if ((s = norm_out_run(&q, stream, h->err_dev)) != MOE_OK) return fail(h, s, "output norm");
     if (!last && !fuse) {
       const moe_block &nb = blocks[i + 1];
-      s = moe_norm_in(res, MOE_F32, D, nb.norm_in_w, nb.norm_dtype, nb.norm_in_eps, nb.unit_offset, a, g.act_dtype, D,
-                      n_tokens, D, stream);
+      s = norm_in_run(res, MOE_F32, D, nb.norm_in_w, nb.norm_dtype, nb.norm_in_eps, nb.unit_offset, a, g.act_dtype, D,
+                      n_tokens, D, stream, h->err_dev);
       if (s != MOE_OK) return fail(h, s, "input norm");
     }
   }

@@ -19,6 +19,14 @@ struct BlockWord {
 };
 cudaError_t block_word(BlockWord *w);
 
+// The operators' entries with an error word of the caller's (norms.cu, ffn.cu): a bounded wait that runs out
+// sets it in place of the device's.
+moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype, float eps,
+                       int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride, int32_t n_tokens, int32_t d_model,
+                       void *stream, uint32_t *err);
+moe_status norm_out_run(const moe_norm_out_args *args, void *stream, uint32_t *err);
+moe_status ffn_forward_run(const moe_ffn_args *args, void *stream, uint32_t *err);
+
 // Clock cycles that a wait of a bulk-copy ring (norms.cu, adapters.cu) may take, and for which a ring's
 // first copies are held back (norms.cu): none, but where a test has the waits run out.
 struct RingSpin {

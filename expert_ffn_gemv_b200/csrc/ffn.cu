@@ -44,7 +44,7 @@ struct GemmArgs {
   CUtensorMap map[kMaxMaps];
   GemmProb p[kMaxProb];    // p[0] is dealt out first, then the others as one list
   int n_prob, bn;          // bn: columns of a tile (swiglu: bn / 2 of g and of u)
-  uint32_t *err;           // set where a bounded wait ran out
+  uint32_t *err;           // set where a bounded wait ran out (NULL at the launch: the device's word)
   // gated epilogues: n columns of f values
   float *g, *u;                // swiglu: saved unless NULL; dswiglu: read
   __nv_bfloat16 *h, *dg, *du;  // swiglu: h; dswiglu: all three
@@ -981,10 +981,12 @@ template <int EPI>
 cudaError_t launch_gemm(GemmArgs &a, const FfnDevice &dev, cudaStream_t st, bool split = true) {
   const Form f = choose_form<EPI>(a.p, a.n_prob, dev, split);
   a.bn = f.bn;
-  BlockWord word;
-  const cudaError_t e = block_word(&word);
-  if (e != cudaSuccess) return e;
-  a.err = word.dev;
+  if (!a.err) {
+    BlockWord word;
+    const cudaError_t e = block_word(&word);
+    if (e != cudaSuccess) return e;
+    a.err = word.dev;
+  }
   const int cols = EPI == kEpiSwiglu ? f.bn / 2 : f.bn;
   int tiles = 0;
   for (int i = 0; i < a.n_prob; ++i) {
@@ -1032,7 +1034,8 @@ extern "C" uint64_t moe_ffn_workspace(int32_t n_tokens, int32_t d_model, int32_t
   return backward ? 3 * nf : nf;
 }
 
-extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
+namespace moe {
+moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
   if (!p || p->struct_size != sizeof(moe_ffn_args)) return MOE_ERR_INVALID_ARGUMENT;
   const int n = p->n_tokens, d = p->d_model, f = p->d_ff;
   if (bad_shape(n, d, f) || bad_act(p->x, p->x_stride, d, n, 2) || bad_mat(p->w_gate) || bad_mat(p->w_up) ||
@@ -1071,7 +1074,7 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     q.b[0] = m.add(p->w_gate, f, d, d, 64);
     q.b[1] = m.add(p->w_up, f, d, d, 64);
     a.h = h, a.g = static_cast<float *>(p->save_gate), a.u = static_cast<float *>(p->save_up);
-    a.f_ld = f;
+    a.f_ld = f, a.err = err;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
   if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
@@ -1083,11 +1086,15 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) {
     q.b[0] = m.add(p->w_down, d, f, f, 64);
     q.out = p->y, q.ld = p->y_stride, q.out_bf16 = p->y_dtype == MOE_BF16;
     q.add = p->add, q.add_ld = p->add_stride, q.add_bf16 = p->add_dtype == MOE_BF16;
+    b.err = err;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
   e = launch_gemm<kEpiPlain>(b, dev, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
+}  // namespace moe
+
+extern "C" moe_status moe_ffn_forward(const moe_ffn_args *p, void *stream) { return ffn_forward_run(p, stream, nullptr); }
 
 extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) {
   if (!p || p->struct_size != sizeof(moe_ffn_bwd_args)) return MOE_ERR_INVALID_ARGUMENT;

@@ -696,7 +696,7 @@ moe_status check_gate(const void *gate, int kind, int act, int dt, int64_t ld, i
   return MOE_OK;
 }
 
-// The ring of a kernel over n rows, or stages = 0 where it does not pay: rows that are not whole
+// The ring of a kernel over n rows (word: where its errors go, the device's if NULL), or stages = 0 where it does not pay: rows that are not whole
 // 16-byte vectors, too long for two stages, or (backward) for the registers, or fewer than kRingRows
 // for each of the blocks that fill the device (1,180 x 2,048, fp32: 12.5 us against 10.5; 8,192 x
 // 4,096, bf16 with a gate of its own: 57 against 97).
@@ -705,7 +705,7 @@ struct RingPlan {
   Ring r{};
   int blocks = 0, threads = 0, smem = 0;
   cudaError_t err = cudaSuccess;
-  RingPlan(std::initializer_list<RowSource> src, int n, int d, int v, bool backward) {
+  RingPlan(std::initializer_list<RowSource> src, int n, int d, int v, bool backward, uint32_t *word) {
     if (v != 8) return;
     for (const RowSource &s : src)
       if (s.p) r.src[r.n_src++] = s, r.stage_bytes += d * (s.bf16 ? 2 : 4);
@@ -724,9 +724,12 @@ struct RingPlan {
     int stages = (kRingBytes / per_sm - 1024) / r.stage_bytes;
     if (stages > kRingMaxStages) stages = kRingMaxStages;
     r.spin = ring_spin();
-    BlockWord word;
-    if ((err = block_word(&word)) != cudaSuccess) return;
-    r.err = word.dev;
+    r.err = word;
+    if (!word) {
+      BlockWord own;
+      if ((err = block_word(&own)) != cudaSuccess) return;
+      r.err = own.dev;
+    }
     blocks = per_sm * nsm;
     smem = 128 + stages * r.stage_bytes;
     if (stages >= 2) r.stages = stages;
@@ -760,10 +763,10 @@ cudaError_t configure_rings() {
   return cudaSuccess;
 }
 
-moe_status launch_fwd(const NormFwd &a, int n, int v, cudaStream_t st) {
+moe_status launch_fwd(const NormFwd &a, int n, int v, cudaStream_t st, uint32_t *err) {
   const bool full = a.gate_kind == MOE_GATE_FULL;
   const RingPlan p({{a.res, a.res_ld, a.res_bf16}, {a.o, a.o_ld, a.o_bf16}, {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, n,
-                   a.d, v, false);
+                   a.d, v, false, err);
   cudaError_t e = p.err;
   if (e == cudaSuccess && p.r.stages) {
     e = configure_rings();
@@ -791,7 +794,7 @@ moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf
                    cudaStream_t st) {
   const bool full = a.gate_kind == MOE_GATE_FULL;
   const RingPlan p({{a.x, a.x_ld, a.x_bf16}, {a.dy, a.dy_ld, a.dy_bf16}, {a.dres, a.dres_ld, a.dres_bf16},
-                    {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, a.n, a.d, v, true);
+                    {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, a.n, a.d, v, true, nullptr);
   int blocks = p.blocks;
   if (p.err != cudaSuccess || (!p.r.stages && bwd_blocks(a.n, &blocks) != cudaSuccess)) return MOE_ERR_CUDA;
   const int sums = (dw ? 1 : 0) + (dg ? 1 : 0);
@@ -874,9 +877,10 @@ extern "C" moe_status moe_debug_set_ring_spin_limit(uint64_t cycles) {
   return MOE_OK;
 }
 
-extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype,
-                                  float eps, int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride,
-                                  int32_t n_tokens, int32_t d_model, void *stream) {
+namespace moe {
+moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype, float eps,
+                       int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride, int32_t n_tokens, int32_t d_model,
+                       void *stream, uint32_t *err) {
   if (n_tokens < 1 || d_model < 1 || !weight || !(eps >= 0.f) || unit_offset < 0 || unit_offset > 1 ||
       bad_rows(x, x_stride, d_model, n_tokens, x_dtype) || bad_rows(h, h_stride, d_model, n_tokens, h_dtype) ||
       bad_vec(weight, w_dtype))
@@ -889,10 +893,10 @@ extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stri
   a.d = d_model, a.inv_d = 1.f / d_model;
   VecRule v(d_model);
   v.row(x, x_stride, a.res_bf16), v.row(h, h_stride, a.h_bf16), v.row(weight, 0, a.w_bf16);
-  return launch_fwd(a, n_tokens, v.v, static_cast<cudaStream_t>(stream));
+  return launch_fwd(a, n_tokens, v.v, static_cast<cudaStream_t>(stream), err);
 }
 
-extern "C" moe_status moe_norm_out(const moe_norm_out_args *p, void *stream) {
+moe_status norm_out_run(const moe_norm_out_args *p, void *stream, uint32_t *err) {
   if (!p || p->struct_size != sizeof(moe_norm_out_args)) return MOE_ERR_INVALID_ARGUMENT;
   const int n = p->n_tokens, d = p->d_model;
   if (n < 1 || d < 1 || bad_rows(p->o, p->o_stride, d, n, p->o_dtype) ||
@@ -920,8 +924,17 @@ extern "C" moe_status moe_norm_out(const moe_norm_out_args *p, void *stream) {
   v.row(a.h, a.h_ld, a.h_bf16), v.row(a.w, 0, a.w_bf16), v.row(a.next_w, 0, a.w_bf16);
   if (a.gate_kind == MOE_GATE_FULL) v.row(a.gate, a.gate_ld, a.gate_bf16);
   if (a.gate_kind == MOE_GATE_CHANNEL) v.row(a.gate, 0, a.gate_bf16);
-  return launch_fwd(a, n, v.v, static_cast<cudaStream_t>(stream));
+  return launch_fwd(a, n, v.v, static_cast<cudaStream_t>(stream), err);
 }
+}  // namespace moe
+
+extern "C" moe_status moe_norm_in(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype,
+                                  float eps, int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride,
+                                  int32_t n_tokens, int32_t d_model, void *stream) {
+  return norm_in_run(x, x_dtype, x_stride, weight, w_dtype, eps, unit_offset, h, h_dtype, h_stride, n_tokens, d_model, stream, nullptr);
+}
+
+extern "C" moe_status moe_norm_out(const moe_norm_out_args *p, void *stream) { return norm_out_run(p, stream, nullptr); }
 
 // Two sums of a row of d values for every block that a backward grid can have.
 extern "C" uint64_t moe_norm_workspace(int32_t n_tokens, int32_t d_model) {

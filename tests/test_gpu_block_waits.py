@@ -102,3 +102,34 @@ def test_check_waits_for_every_stream(P, limit):
         assert not side.query()
         assert P.block_check() == status
         assert side.query()
+
+
+def test_a_run_of_layers_reports_by_its_handle(P, limit):
+    """The norm behind the experts waits in a ring; the one before them, whose weight is off a 16-byte boundary,
+    has none, so that the experts see sound values."""
+    import synth
+    from helpers import load_layer_device, moe_for
+
+    wl = synth.small_workload(d_model=512, d_ff=256, n_experts=32, top_k=4, n_shared=1, shared_d_ff=256)
+    n = 2000
+    m = moe_for(wl, 1, n, seed=3)
+    load_layer_device(m, 0, wl, 3, 0)
+    w = randn(513, seed=1, std=0.2, mean=1.0)[1:]
+    x, out = randn(n, 512, seed=2, dtype=BF), torch.empty((n, 512), device="cuda")
+    run = lambda: m.forward_blocks(0, [P.Block(norm_in=w)], x, out)
+    run()
+    torch.cuda.synchronize()
+    assert m.check() == P.MOE_OK
+    want = out.clone()
+    limit(2_000_000)
+    run()
+    limit(0)
+    torch.cuda.synchronize()
+    assert P.block_check() == P.MOE_OK
+    with pytest.raises(P.MoeError) as e:
+        run()
+    assert e.value.status == P.MOE_ERR_TIMEOUT
+    run()
+    torch.cuda.synchronize()
+    assert m.check() == P.MOE_OK and torch.equal(out, want)
+    m.close()
