@@ -198,7 +198,8 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, need_dx=True, need_dw=Tr
 
 
 def block_check() -> int:
-    """Waits for the current device; MOE_ERR_TIMEOUT if a wait of the norms' or the dense block's kernels ran out."""
+    """Waits for the current device, all its streams; MOE_ERR_TIMEOUT if a wait of the norms' or the dense block's
+    kernels ran out there (without it, the next call of one of them raises that)."""
     return _lib.moe_block_check()
 
 

@@ -18,9 +18,11 @@ struct BlockWord {
   uint32_t *host = nullptr, *dev = nullptr;
 };
 cudaError_t block_word(BlockWord *w);
+// MOE_ERR_TIMEOUT, once, where a kernel of an earlier call on this device set its word.
+moe_status block_pending();
 
 // The operators' entries with an error word of the caller's (norms.cu, ffn.cu): a bounded wait that runs out
-// sets it in place of the device's.
+// sets it in place of the device's, and the device's is not asked for what earlier calls left there.
 moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const void *weight, int32_t w_dtype, float eps,
                        int32_t unit_offset, void *h, int32_t h_dtype, int64_t h_stride, int32_t n_tokens, int32_t d_model,
                        void *stream, uint32_t *err);

@@ -1046,6 +1046,7 @@ moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
       (p->save_gate != nullptr) != (p->save_up != nullptr) || (p->save_gate && (bad_mat(p->save_gate) || bad_mat(p->save_up))) ||
       bad_mat(p->workspace) || p->workspace_bytes < moe_ffn_workspace(n, d, f, 0))
     return MOE_ERR_INVALID_ARGUMENT;
+  if (const moe_status s = err ? MOE_OK : block_pending()) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(p->workspace);
   cudaError_t e;
@@ -1106,6 +1107,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
       (!p->dx && !p->dw_gate && !p->dw_down) || bad_mat(p->workspace) ||
       p->workspace_bytes < moe_ffn_workspace(n, d, f, 1))
     return MOE_ERR_INVALID_ARGUMENT;
+  if (const moe_status s = block_pending()) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   FfnDevice dev{};
   cudaError_t e;

@@ -841,30 +841,43 @@ RingSpin ring_spin() {
   return v ? RingSpin{v, 4 * v} : RingSpin{kRingSpin, 0};
 }
 
+namespace {
+constexpr int kMaxDevices = 64, kWordBytes = 64;
+std::atomic<char *> g_words{nullptr};            // the words of all devices
+std::atomic<char *> g_words_seen[kMaxDevices];   // the same as each device sees them
+}  // namespace
+
+moe_status block_pending() {
+  char *page = g_words.load(std::memory_order_acquire);
+  int dev = 0;
+  if (!page || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return MOE_OK;
+  uint32_t *w = reinterpret_cast<uint32_t *>(page + dev * kWordBytes);
+  if (!__atomic_load_n(w, __ATOMIC_RELAXED)) return MOE_OK;
+  return __atomic_exchange_n(w, 0u, __ATOMIC_ACQ_REL) ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
 cudaError_t block_word(BlockWord *w) {
-  constexpr int kMaxDevices = 64, kWordBytes = 64;
   static std::mutex mutex;
-  static char *page = nullptr;
-  static std::atomic<char *> known[kMaxDevices];  // the page as the device sees it
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices) return cudaErrorNotSupported;
-  char *seen = known[dev].load(std::memory_order_acquire);
+  char *seen = g_words_seen[dev].load(std::memory_order_acquire), *page = g_words.load(std::memory_order_acquire);
   if (!seen) {
     std::lock_guard<std::mutex> lock(mutex);
+    page = g_words.load(std::memory_order_acquire);
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // this allocation is no part of any capture
     if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
     if (!page) {
       void *p = nullptr;
       e = cudaHostAlloc(&p, kMaxDevices * kWordBytes, cudaHostAllocMapped | cudaHostAllocPortable);
-      if (e == cudaSuccess) page = static_cast<char *>(memset(p, 0, kMaxDevices * kWordBytes));
+      if (e == cudaSuccess) g_words.store(page = static_cast<char *>(memset(p, 0, kMaxDevices * kWordBytes)), std::memory_order_release);
     }
     void *p = nullptr;
     if (e == cudaSuccess) e = cudaHostGetDevicePointer(&p, page, 0);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
-    known[dev].store(seen = static_cast<char *>(p), std::memory_order_release);
+    g_words_seen[dev].store(seen = static_cast<char *>(p), std::memory_order_release);
   }
   w->host = reinterpret_cast<uint32_t *>(page + dev * kWordBytes);
   w->dev = reinterpret_cast<uint32_t *>(seen + dev * kWordBytes);
@@ -886,6 +899,7 @@ moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const v
       bad_vec(weight, w_dtype))
     return MOE_ERR_INVALID_ARGUMENT;
   if (d_model > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  if (const moe_status s = err ? MOE_OK : block_pending()) return s;
   NormFwd a{};
   a.res = x, a.res_ld = x_stride, a.res_bf16 = x_dtype == MOE_BF16;
   a.next_w = weight, a.w_bf16 = w_dtype == MOE_BF16, a.next_eps = eps, a.w_off = static_cast<float>(unit_offset);
@@ -908,6 +922,7 @@ moe_status norm_out_run(const moe_norm_out_args *p, void *stream, uint32_t *err)
   const moe_status gs = check_gate(p->gate, p->gate_kind, p->gate_act, p->gate_dtype, p->gate_stride, d, n);
   if (gs != MOE_OK) return gs;
   if (d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  if (const moe_status s = err ? MOE_OK : block_pending()) return s;
   NormFwd a{};
   a.o = p->o, a.o_ld = p->o_stride, a.o_bf16 = p->o_dtype == MOE_BF16;
   a.res = p->residual, a.res_ld = p->res_stride, a.res_bf16 = p->res_dtype == MOE_BF16;
@@ -956,6 +971,7 @@ extern "C" moe_status moe_norm_in_backward(const moe_norm_in_bwd_args *p, void *
       p->unit_offset < 0 || p->unit_offset > 1 || !(p->eps >= 0.f))
     return MOE_ERR_INVALID_ARGUMENT;
   if (d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  if (const moe_status s = block_pending()) return s;
   NormBwd a{};
   a.x = p->x, a.x_ld = p->x_stride, a.x_bf16 = p->x_dtype == MOE_BF16;
   a.dy = p->dh, a.dy_ld = p->dh_stride, a.dy_bf16 = p->dh_dtype == MOE_BF16;
@@ -983,6 +999,7 @@ extern "C" moe_status moe_norm_out_backward(const moe_norm_out_bwd_args *p, void
     gs = check_gate(p->dgate, p->gate_kind, p->gate_act, p->gate_dtype, p->dgate_stride, d, n);
   if (gs != MOE_OK) return gs;
   if (d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+  if ((gs = block_pending()) != MOE_OK) return gs;
   NormBwd a{};
   a.x = p->o, a.x_ld = p->o_stride, a.x_bf16 = p->o_dtype == MOE_BF16;
   a.dy = p->dres, a.dy_ld = p->dres_stride, a.dy_bf16 = p->dres_dtype == MOE_BF16;

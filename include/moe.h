@@ -202,9 +202,10 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
  * Outputs may not overlap inputs unless said so.
  * ------------------------------------------------------------------------------------------- */
-/* Waits for the current device, all its streams, and returns (and clears) a pending MOE_ERR_TIMEOUT of
- * the norms' and the dense block's kernels there, whoever called them: a bounded wait ran out and the
- * results of a call are not valid. */
+/* A bounded wait of the norms' or the dense block's kernels that ran out makes the next call of one of
+ * them on that device, whoever made the first, return MOE_ERR_TIMEOUT, once and with nothing launched:
+ * the results of an earlier call are not valid.  moe_block_check waits for the current device, all its
+ * streams, and returns (and clears) what is pending there. */
 moe_status moe_block_check(void);
 
 /* What a gate is broadcast over: one value per column, per token, or of its own for every value. */

@@ -133,3 +133,27 @@ def test_a_run_of_layers_reports_by_its_handle(P, limit):
     torch.cuda.synchronize()
     assert m.check() == P.MOE_OK and torch.equal(out, want)
     m.close()
+
+
+def test_the_next_call_reports(P, limit):
+    """Once, whichever of the operators it is, and with nothing launched."""
+    x, w = randn(2000, 1024, seed=1), randn(1024, seed=2)
+    a, m = randn(12, 64, seed=3, dtype=BF), randn(64, 64, seed=4, dtype=BF)
+    y, saved = P.ffn_forward(a, m, m, m, save=True)
+    out = torch.full((3, 64), 7.0, device="cuda")
+    calls = {"norm_in": lambda: P.norm_in(x[:3, :64], w[:64], out=out), "norm_out": lambda: P.norm_out(x[:3, :64], x[:3, :64], out=out),
+             "norm_in_backward": lambda: P.norm_in_backward(x, w, x), "norm_out_backward": lambda: P.norm_out_backward(x, x),
+             "ffn_forward": lambda: P.ffn_forward(a[:3], m, m, m, out=out), "ffn_backward": lambda: P.ffn_backward(y, a, m, m, m, saved)}
+    for name, call in calls.items():
+        limit(2_000_000)
+        P.norm_in(x, w)
+        limit(0)
+        torch.cuda.synchronize()
+        with pytest.raises(P.MoeError) as e:
+            call()
+        assert e.value.status == P.MOE_ERR_TIMEOUT and name in str(e.value)
+        torch.cuda.synchronize()
+        assert (out == 7).all()
+    for call in calls.values():
+        call()
+    assert P.block_check() == P.MOE_OK
