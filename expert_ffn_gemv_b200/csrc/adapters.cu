@@ -811,6 +811,10 @@ bool host_ptr(const void *p) {
 
 }  // namespace
 
+namespace moe {
+moe_status adapters_pending(moe_adapters *h) { return ad_pending(h); }
+}  // namespace moe
+
 extern "C" {
 
 moe_status moe_adapters_create(const moe_adapters_config *cfg, moe_adapters **out) {
@@ -927,6 +931,14 @@ moe_status moe_adapters_load(moe_adapters *h, int32_t slot, const void *a, const
 moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, int64_t x_stride, const void *base,
                               int64_t base_stride, void *out, int64_t out_stride, int32_t out_dtype, const int32_t *ids,
                               int32_t n_tokens, void *stream) {
+  return adapters_run(h, x, x_dtype, x_stride, base, base_stride, out, out_stride, out_dtype, ids, n_tokens, stream, true);
+}
+
+}  // extern "C"
+
+moe_status moe::adapters_run(moe_adapters *h, const void *x, int32_t x_dtype, int64_t x_stride, const void *base,
+                             int64_t base_stride, void *out, int64_t out_stride, int32_t out_dtype, const int32_t *ids,
+                             int32_t n_tokens, void *stream, bool pending) {
   if (!h) return MOE_ERR_INVALID_ARGUMENT;
   const moe_adapters_config &g = h->cfg;
   if (!x || !base || !out || !ids || n_tokens < 1 || n_tokens > g.max_tokens || (x_dtype != MOE_F32 && x_dtype != MOE_BF16) ||
@@ -941,8 +953,7 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
     return ad_fail(h, MOE_ERR_INVALID_ARGUMENT, "a row stride is smaller than a row");
   if (base == out && n_tokens > 1 && base_stride != out_stride)
     return ad_fail(h, MOE_ERR_INVALID_ARGUMENT, "out is base with another row stride");
-  moe_status s = ad_pending(h);
-  if (s != MOE_OK) return s;
+  if (const moe_status s = pending ? ad_pending(h) : MOE_OK) return s;
   Device dev(g.device);
   if (!dev.ok) return ad_fail(h, MOE_ERR_CUDA, "set device");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -975,5 +986,3 @@ moe_status moe_adapters_apply(moe_adapters *h, const void *x, int32_t x_dtype, i
   });
   return e == cudaSuccess ? MOE_OK : ad_cuda(h, e, "adapter launch");
 }
-
-}  // extern "C"

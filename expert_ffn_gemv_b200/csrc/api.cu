@@ -722,6 +722,9 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
   if (s != MOE_OK) return s;
   for (int l = first_layer; l < first_layer + n_layers; ++l)
     if (!h->layers[l].loaded) return fail(h, MOE_ERR_NOT_LOADED, "layer not loaded");
+  for (int i = 0; i < n_layers; ++i)
+    if (blocks[i].adapters && (s = adapters_pending(blocks[i].adapters)) != MOE_OK)
+      return fail(h, s, std::string("adapters: ") + moe_adapters_last_error(blocks[i].adapters));
   // the block input a and the block output o (fp32) take the staging buffers, x the residual buffer
   void *a = h->x_stage;
   float *o = static_cast<float *>(h->y_stage), *res = h->res[0];
@@ -746,7 +749,7 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
       if ((s = ffn_forward_run(&f, stream, h->err_dev)) != MOE_OK) return fail(h, s, "dense block");
     }
     if (b.adapters) {
-      s = moe_adapters_apply(b.adapters, a, g.act_dtype, D, o, D, o, D, MOE_F32, adapter_ids, n_tokens, stream);
+      s = adapters_run(b.adapters, a, g.act_dtype, D, o, D, o, D, MOE_F32, adapter_ids, n_tokens, stream, false);
       if (s != MOE_OK) return fail(h, s, std::string("adapters: ") + moe_adapters_last_error(b.adapters));
     }
     moe_norm_out_args q{};

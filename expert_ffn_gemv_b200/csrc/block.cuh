@@ -10,6 +10,13 @@ namespace moe {
 
 // Whether the handle adapts d -> d on this device and takes n tokens a call (adapters.cu).
 bool adapters_match(const moe_adapters *h, int d, int device, int n);
+// What kernels of earlier calls on the handle reported, once; and moe_adapters_apply without asking for it
+// (adapters.cu): a run of layers asks before its first launch, since what a layer of the run itself
+// reports may or may not be there when the next one is enqueued.
+moe_status adapters_pending(moe_adapters *h);
+moe_status adapters_run(moe_adapters *h, const void *x, int32_t x_dtype, int64_t x_stride, const void *base, int64_t base_stride,
+                        void *out, int64_t out_stride, int32_t out_dtype, const int32_t *ids, int32_t n_tokens, void *stream,
+                        bool pending);
 
 // The current device's error word of the norms and the dense block: host memory that kernels write, so
 // that the host can read and clear it in one step (norms.cu).  A first use allocates the words of all

@@ -371,7 +371,9 @@ uint64_t moe_blocks_workspace(const moe_handle *h, const moe_block *blocks, int3
 /* x_in: act_dtype, x_out: out_dtype, device memory, not aliased.  adapter_ids: n_tokens slots, or NULL
  * when no layer has adapters.  A dense block needs act_dtype = MOE_BF16.  Errors as
  * moe_forward_stack, and those of the operators; a bounded wait that runs out in any kernel of the run
- * but the adapters' is reported by the next call on h (or moe_check), not by moe_block_check. */
+ * but the adapters' is reported by the next call on h (or moe_check), not by moe_block_check.  What
+ * the adapters' kernels of earlier calls reported is returned before anything is launched; an id that
+ * is out of range in this run counts as -1 in all its layers and is reported by a later call. */
 moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_layers, const moe_block *blocks,
                               const void *x_in, void *x_out, int32_t n_tokens, const int32_t *adapter_ids,
                               void *workspace, uint64_t workspace_bytes, void *stream, moe_route_out *per_layer_route);

@@ -192,3 +192,32 @@ def test_refusals(P, model):
         kw = {**dict(blocks=b, x_in=x, x_out=out, adapter_ids=ids), **bad}
         with pytest.raises(ValueError):
             m.forward_blocks(0, **kw)
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_ids_out_of_range_in_a_run(P, model, n):
+    """A run of layers that share a handle takes them as -1 throughout, however far the device has got; the
+    next run returns the error before anything of it is launched."""
+    wl, m, ad = model
+    blocks = blocks_of(P, ad)
+    x, out = randn(n, D, seed=1, dtype=BF), torch.empty((n, D), device="cuda")
+    ids = (torch.arange(n) % 5 - 1).to(torch.int32).cuda()
+    want = torch.empty_like(out)
+    m.forward_blocks(0, blocks, x, want, adapter_ids=ids)
+    ids[ids == -1] = 77
+    for _ in range(5):  # the first layer's report may come before or after the third layer's launch
+        m.forward_blocks(0, blocks, x, out, adapter_ids=ids)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and ad.check() == P.MOE_ERR_DEVICE_FAULT and ad.check() == P.MOE_OK
+    m.forward_blocks(0, blocks, x, out, adapter_ids=ids)
+    torch.cuda.synchronize()
+    out.fill_(7)
+    routes = [{k: v.fill_(-5) for k, v in route_buffers(n, wl.top_k, wl.n_experts).items()} for _ in range(2)]
+    with pytest.raises(P.MoeError) as e:  # only the second layer of this run has the adapters
+        m.forward_blocks(1, blocks[1:], x, out, adapter_ids=ids, routes=routes)
+    assert e.value.status == P.MOE_ERR_DEVICE_FAULT and "adapter id" in str(e.value)
+    torch.cuda.synchronize()
+    assert (out == 7).all() and all((v == -5).all() for r in routes for v in r.values())
+    m.forward_blocks(0, blocks, x, out, adapter_ids=ids)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and ad.check() == P.MOE_ERR_DEVICE_FAULT
