@@ -712,12 +712,27 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
       return fail(h, MOE_ERR_INVALID_ARGUMENT, "bad block description");
     if (b.ffn_d_ff && (g.act_dtype != MOE_BF16 || !b.ffn_gate || !b.ffn_up || !b.ffn_down))
       return fail(h, MOE_ERR_INVALID_ARGUMENT, "a dense block needs bf16 activations and its three matrices");
+    // what the operators would refuse, before any of them is enqueued
+    const uintptr_t mask = b.norm_dtype == MOE_BF16 ? 1 : 3;
+    for (const void *p : {b.norm_in_w, b.norm_out_w, b.gate})
+      if (reinterpret_cast<uintptr_t>(p) & mask) return fail(h, MOE_ERR_INVALID_ARGUMENT, "a norm weight or gate is not aligned to its type");
+    if (!(b.norm_in_eps >= 0.f) || (b.norm_out_w && !(b.norm_out_eps >= 0.f)) || b.unit_offset < 0 || b.unit_offset > 1 ||
+        (b.gate && b.gate_act != MOE_GATE_LINEAR && b.gate_act != MOE_GATE_SIGMOID))
+      return fail(h, MOE_ERR_INVALID_ARGUMENT, "bad eps, unit_offset or gate_act");
+    if (b.ffn_d_ff && (bad_ffn_dim(b.ffn_d_ff) || !aligned16(b.ffn_gate) || !aligned16(b.ffn_up) || !aligned16(b.ffn_down)))
+      return fail(h, MOE_ERR_INVALID_ARGUMENT, "a dense block's d_ff is no multiple of 8 up to 65536, or a matrix is not 16-byte aligned");
     if (b.adapters && !adapter_ids) return fail(h, MOE_ERR_INVALID_ARGUMENT, "adapter_ids is missing");
     if (b.adapters && !adapters_match(b.adapters, D, g.device, n_tokens))
       return fail(h, MOE_ERR_INVALID_ARGUMENT, "the adapters' sizes, device or max_tokens do not fit");
   }
-  if (workspace_bytes < moe_blocks_workspace(h, blocks, n_layers, n_tokens))
-    return fail(h, MOE_ERR_INVALID_ARGUMENT, "workspace too small");
+  if (D > kNormMaxD) return fail(h, MOE_ERR_UNSUPPORTED, "norms of more than 8192 columns");
+  const uint64_t need = moe_blocks_workspace(h, blocks, n_layers, n_tokens);
+  if (workspace_bytes < need || (need && (!workspace || !aligned16(workspace))))
+    return fail(h, MOE_ERR_INVALID_ARGUMENT, "workspace too small or not 16-byte aligned");
+  const uintptr_t in_mask = g.act_dtype == MOE_BF16 ? 1 : 3, out_mask = g.out_dtype == MOE_BF16 ? 1 : 3;
+  if (reinterpret_cast<uintptr_t>(x_in) & in_mask || reinterpret_cast<uintptr_t>(x_out) & out_mask ||
+      reinterpret_cast<uintptr_t>(adapter_ids) & 3)
+    return fail(h, MOE_ERR_INVALID_ARGUMENT, "x_in, x_out or adapter_ids is not aligned to its type");
   moe_status s = check_device_error(h, st);
   if (s != MOE_OK) return s;
   for (int l = first_layer; l < first_layer + n_layers; ++l)

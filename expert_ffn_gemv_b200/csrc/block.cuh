@@ -36,6 +36,11 @@ moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const v
 moe_status norm_out_run(const moe_norm_out_args *args, void *stream, uint32_t *err);
 moe_status ffn_forward_run(const moe_ffn_args *args, void *stream, uint32_t *err);
 
+// Limits that they check.
+constexpr int kNormMaxD = 8192;
+constexpr int kFfnMaxDim = 65536;
+inline bool bad_ffn_dim(int v) { return v < 8 || v % 8 || v > kFfnMaxDim; }
+
 // Clock cycles that a wait of a bulk-copy ring (norms.cu, adapters.cu) may take, and for which a ring's
 // first copies are held back (norms.cu): none, but where a test has the waits run out.
 struct RingSpin {

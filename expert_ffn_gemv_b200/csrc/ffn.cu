@@ -1016,13 +1016,13 @@ cudaError_t launch_small(const SmallArgs &s, cudaStream_t st) {
   return e == cudaSuccess ? cudaLaunchKernelEx(&d.cfg, k_ffn_down, s, cd) : e;
 }
 
-constexpr int kMaxDim = 65536, kMaxRows = 1 << 20;  // at most 2^23 tiles
+constexpr int kMaxRows = 1 << 20;  // at most 2^23 tiles
 bool bad_mat(const void *p) { return !p || !aligned16(p); }
 bool bad_act(const void *p, int64_t ld, int d, int n, int bytes) {
   return !p || !aligned16(p) || ld * bytes % 16 || (n > 1 && ld < d);
 }
 bool bad_shape(int n, int d, int f) {
-  return n < 1 || n > kMaxRows || d < 8 || d % 8 || d > kMaxDim || f < 8 || f % 8 || f > kMaxDim;
+  return n < 1 || n > kMaxRows || bad_ffn_dim(d) || bad_ffn_dim(f);
 }
 uint64_t align_ws(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 

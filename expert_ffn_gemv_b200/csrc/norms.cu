@@ -28,8 +28,6 @@
 namespace moe {
 namespace {
 
-constexpr int kNormMaxD = 8192;  // V * NCH * threads
-
 // V consecutive values (V = 1, 2, 4 or 8: the widest that width, pointers and strides allow)
 template <int V>
 __device__ __forceinline__ void load_v(const void *p, int64_t i, int bf16, float (&v)[V]) {
@@ -109,7 +107,7 @@ __device__ __forceinline__ void store_v(void *p, int64_t i, int bf16, float (&v)
   }
 }
 
-// A thread's values of a row: columns (256 c + thread) V .. + V - 1, c < NCH, below d.  (A block of
+// A thread's values of a row: columns (256 c + thread) V .. + V - 1, c < NCH, below d <= kNormMaxD.  (A block of
 // fewer threads holds its row in c = 0.)  One branch on the type for all of a row's loads.
 constexpr int kNormMaxThreads = 256;
 template <int V, int NCH>

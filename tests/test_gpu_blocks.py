@@ -221,3 +221,37 @@ def test_ids_out_of_range_in_a_run(P, model, n):
     m.forward_blocks(0, blocks, x, out, adapter_ids=ids)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and ad.check() == P.MOE_ERR_DEVICE_FAULT
+
+
+def test_a_bad_second_layer_is_refused_before_the_first_is_launched(P, model):
+    wl, m, ad = model
+    n = 9
+    w = randn(D, seed=20, std=0.2, mean=1.0)
+    x, out = randn(n, D, seed=1, dtype=BF), torch.full((n, D), 7.0, device="cuda")
+    mats = [randn(320 * D + 8, seed=30 + i, std=0.05, dtype=BF) for i in range(3)]
+    ffn = [t[:320 * D].view(s) for t, s in zip(mats, ((320, D), (320, D), (D, 320)))]
+    off = [t[1:320 * D + 1].view(s) for t, s in zip(mats, ((320, D), (320, D), (D, 320)))]  # 2 bytes on
+    odd = [t[:12 * D].view(s) for t, s in zip(mats, ((12, D), (12, D), (D, 12)))]
+    blocks = [P.Block(norm_in=w, ffn=(off[0], ffn[1], ffn[2])), P.Block(norm_in=w, ffn=(ffn[0], off[1], ffn[2])),
+              P.Block(norm_in=w, ffn=(ffn[0], ffn[1], off[2])), P.Block(norm_in=w, ffn=tuple(odd)),
+              P.Block(norm_in=w, eps=-1.0), P.Block(norm_in=w, eps=float("nan")), P.Block(norm_in=w, unit_offset=2),
+              P.Block(norm_in=w, unit_offset=-1)]
+    routes = [{k: v.fill_(-5) for k, v in route_buffers(n, wl.top_k, wl.n_experts).items()} for _ in range(2)]
+    for b in blocks:
+        with pytest.raises(P.MoeError) as e:
+            m.forward_blocks(0, [P.Block(norm_in=w), b], x, out, routes=routes)
+        assert e.value.status == P.MOE_ERR_INVALID_ARGUMENT
+        torch.cuda.synchronize()
+        assert (out == 7).all() and all((v == -5).all() for r in routes for v in r.values()), b
+    arr = (P.moe_block * 1)(P.Block(norm_in=w, gate=w, ffn=tuple(ffn)).args(D, x.device))
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    run = lambda work: P.lib().moe_forward_blocks(m.h, 0, 1, arr, x.data_ptr(), out.data_ptr(), n, None, work, 1 << 19, 0, None)
+    assert run(ws.data_ptr() + 8) == P.MOE_ERR_INVALID_ARGUMENT and run(None) == P.MOE_ERR_INVALID_ARGUMENT
+    arr[0].gate_act = 2
+    assert run(ws.data_ptr()) == P.MOE_ERR_INVALID_ARGUMENT
+    arr[0].gate_act = 1
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    assert run(ws.data_ptr()) == P.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
