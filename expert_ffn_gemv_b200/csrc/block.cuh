@@ -76,11 +76,15 @@ inline cudaError_t current_sm_count(int *nsm) {
 // 1 / (1 + exp(-z)) by the approximate power and reciprocal, 3 units in the last place off (from z = -88 on
 // down more, to 0; 1 / inf = 0).  Four instructions: an IEEE division takes ten, an exponential that keeps
 // subnormals three more.
-__device__ __forceinline__ float fast_sigmoid(float z) {
-  float e, r;
+__device__ __forceinline__ float fast_sigmoid(float z, float &e) {  // e: exp(-z)
+  float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
+}
+__device__ __forceinline__ float fast_sigmoid(float z) {
+  float e;
+  return fast_sigmoid(z, e);
 }
 
 // D += A B, mma.sync m16n8k16, bf16 operands, fp32 accumulators

@@ -183,6 +183,28 @@ __device__ __forceinline__ void clear_sums(float (&red)[N]) {
 __device__ __forceinline__ float gate_value(float g, int act) {
   return act == MOE_GATE_SIGMOID ? 1.0f / (1.0f + expf(-g)) : g;
 }
+// The slope of the sigmoid is sigmoid(g) sigmoid(-g).  With the second factor as 1 - a nothing would be left
+// where a rounds to 1 (off by 1e-3 at g = 10, 0 from g = 17 on, where the slope is 4e-8), so it comes from
+// the exponential.  Of a token's gate, a = gate_value(g):
+__device__ __forceinline__ float gate_slope(float g, float a, int act) {
+  return act == MOE_GATE_SIGMOID ? a * fminf(expf(-g) * a, 1.0f) : 1.f;  // (infinity times 0 gives 1)
+}
+// Both factors of a value's gate.
+__device__ __forceinline__ void fast_sigmoids(float g, float &a, float &c) {
+  float e;
+  a = fast_sigmoid(g, e);
+  c = fminf(e * a, 1.0f);  // infinity times 0: 1
+}
+// The same of a column's gate, kept in one register for all rows: the smaller factor, with the sign bit set
+// where g is positive.
+__device__ __forceinline__ float fold_sigmoid(float g) {
+  float a, c;
+  fast_sigmoids(g, a, c);
+  return g > 0.f ? -c : a;
+}
+__device__ __forceinline__ float folded_value(float v) { return __float_as_int(v) < 0 ? 1.0f + v : v; }
+__device__ __forceinline__ float folded_slope(float v) { return fmaf(-fabsf(v), fabsf(v), fabsf(v)); }
+
 // 1 / sqrt(sum / d + eps)
 __device__ __forceinline__ float root(float sum, float inv_d, float eps) { return rsqrtf(__fadd_rn(__fmul_rn(sum, inv_d), eps)); }
 
@@ -248,12 +270,15 @@ __device__ __forceinline__ void fwd_row(const NormFwd &a, int64_t t, float (&r)[
   store_row<V, NCH>(a.h, t * a.h_ld, a.h_bf16, d, r);
 }
 
-// a(g) of a token gate, else 1
-__device__ __forceinline__ float token_gate(const void *gate, int kind, int act, int64_t i, int bf16) {
-  if (kind != MOE_GATE_TOKEN) return 1.f;
+// A token gate g and a(g), else 1
+__device__ __forceinline__ float2 token_gates(const void *gate, int kind, int act, int64_t i, int bf16) {
+  if (kind != MOE_GATE_TOKEN) return make_float2(1.f, 1.f);
   float g[1];
   load_v<1>(gate, i, bf16, g);
-  return gate_value(g[0], act);
+  return make_float2(g[0], gate_value(g[0], act));
+}
+__device__ __forceinline__ float token_gate(const void *gate, int kind, int act, int64_t i, int bf16) {
+  return token_gates(gate, kind, act, i, bf16).y;
 }
 
 // One block per token, every load of the row on its way before the first sum.
@@ -288,9 +313,14 @@ struct NormBwd {
   float eps, scale, w_off, inv_d;
 };
 
-// What a block keeps from row to row: the sums over its rows, and (KEEP) the weight and a gate by column.
-template <int V, int NCH, bool KEEP>
+// What a block keeps from row to row: the sums over its rows (a channel gate's without its slope, which
+// comes in at the end), and (KEEP) the weight and a gate by column.  For the slope a sigmoid's two factors are
+// kept folded, or the gate is loaded again at the end.  The second costs up to 1 us (1,177 x 1,001: 12.9 us
+// against 12.2), the first arithmetic in every row, which many rows feel (8,192 x 2,048: 43.5 us against 41),
+// and registers, which cost eight values a thread half their blocks (1,177 x 2,001: 21.9 us against 18.0).
+template <int V, int NCH, bool KEEP, bool RING>
 struct BwdState {
+  static constexpr bool FOLD = KEEP && !RING && V * NCH != 8;
   float dw[NCH][V], dg[NCH][V], w[NCH][V], gc[NCH][V];
   __device__ __forceinline__ explicit BwdState(const NormBwd &a) {
     fill<V, NCH>(dw, 0.f), fill<V, NCH>(dg, 0.f), fill<V, NCH>(w, a.w ? 0.f : 1.f), fill<V, NCH>(gc, 0.f);
@@ -300,10 +330,21 @@ struct BwdState {
     if (a.w) load_weight<V, NCH>(a.w, a.w_bf16, a.d, a.w_off, w);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
       load_row<V, NCH>(a.gate, 0, a.gate_bf16, a.d, gc);
-      gate_values<V, NCH>(gc, a.gate_act);
+      if (FOLD && a.gate_act == MOE_GATE_SIGMOID) {
+        MOE_EACH(c, k) gc[c][k] = fold_sigmoid(gc[c][k]);
+      } else {
+        gate_values<V, NCH>(gc, a.gate_act);
+      }
     }
   }
   __device__ __forceinline__ void finish(const NormBwd &a) {
+    if (a.dg_part && a.gate_act == MOE_GATE_SIGMOID) {
+      if (!FOLD) {
+        load_row<V, NCH>(a.gate, 0, a.gate_bf16, a.d, gc);
+        MOE_EACH(c, k) gc[c][k] = fold_sigmoid(gc[c][k]);
+      }
+      MOE_EACH(c, k) dg[c][k] *= folded_slope(gc[c][k]);
+    }
     if (a.dw_part) store_row<V, NCH>(a.dw_part, static_cast<int64_t>(blockIdx.x) * a.d, 0, a.d, dw);
     if (a.dg_part) store_row<V, NCH>(a.dg_part, static_cast<int64_t>(blockIdx.x) * a.d, 0, a.d, dg);
   }
@@ -313,14 +354,16 @@ struct BwdRow {
   float x[NCH][V], dy[NCH][V], dres[NCH][V], g[NCH][V];
 };
 
-template <int V, int NCH, bool KEEP>
-__device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, NCH> &q, BwdState<V, NCH, KEEP> &st, float gt,
-                                        float *red, int threads) {
+template <int V, int NCH, bool KEEP, bool RING>
+__device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, NCH> &q, BwdState<V, NCH, KEEP, RING> &st,
+                                        float2 token, float *red, int threads) {
   const int d = a.d;
+  const float gt = token.y;
   if (!KEEP) st.columns(a);
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL, full = a.gate_kind == MOE_GATE_FULL;
-  if (full) {
-    gate_values<V, NCH>(q.g, a.gate_act);
+  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID, full_sigmoid = full && sigmoid;
+  if (st.FOLD && channel && sigmoid) {
+    MOE_EACH(c, k) q.g[c][k] = folded_value(st.gc[c][k]);
   } else if (channel) {
     MOE_EACH(c, k) q.g[c][k] = st.gc[c][k];
   }
@@ -331,7 +374,15 @@ __device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, N
     q.dy[c][k] = __fmul_rn(a.scale, q.dy[c][k]);
     s[0] = fmaf(q.x[c][k], q.x[c][k], s[0]);
   }
-  if (by_value) {
+  if (full_sigmoid) {  // leaves s dy a in dy, the slope's other factor in g
+    MOE_EACH(c, k) {
+      float av, other;
+      fast_sigmoids(q.g[c][k], av, other);
+      q.dy[c][k] = __fmul_rn(q.dy[c][k], av);
+      q.g[c][k] = other;
+      s[1] = fmaf(__fmul_rn(q.dy[c][k], st.w[c][k]), q.x[c][k], s[1]);
+    }
+  } else if (by_value) {
     MOE_EACH(c, k) s[1] = fmaf(__fmul_rn(__fmul_rn(q.dy[c][k], q.g[c][k]), st.w[c][k]), q.x[c][k], s[1]);
   } else {
     MOE_EACH(c, k) s[1] = fmaf(__fmul_rn(q.dy[c][k], st.w[c][k]), q.x[c][k], s[1]);
@@ -339,18 +390,24 @@ __device__ __forceinline__ void bwd_row(const NormBwd &a, int64_t t, BwdRow<V, N
   block_sum<2>(s, red, threads);
   const float rt = a.w ? root(s[0], a.inv_d, a.eps) : 1.f;
   const float m = a.w ? (by_value ? s[1] : gt * s[1]) * a.inv_d * (rt * rt) : 0.f;
-  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
   if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
-    float v1[1] = {(sigmoid ? gt * (1.f - gt) : 1.f) * rt * s[1]};
+    float v1[1] = {gate_slope(token.x, gt, a.gate_act) * rt * s[1]};
     store_v<1>(a.dgate, t * a.dgate_ld, a.gate_bf16, v1);
   }
-  // dx in dres, the gate's gradient in g
-  if (by_value) {
+  // dx in dres, the gradient of a value's own gate in g
+  if (full_sigmoid) {
     MOE_EACH(c, k) {
-      const float x = q.x[c][k], av = q.g[c][k], da = __fmul_rn(q.dy[c][k], av);
+      const float x = q.x[c][k], da = q.dy[c][k];
       q.dres[c][k] = __fadd_rn(q.dres[c][k], __fmul_rn(rt, fmaf(-x, m, __fmul_rn(da, st.w[c][k]))));
       st.dw[c][k] = fmaf(da * rt, x, st.dw[c][k]);
-      const float gg = q.dy[c][k] * (x * rt * st.w[c][k]) * (sigmoid ? av * (1.f - av) : 1.f);
+      q.g[c][k] = da * (x * rt * st.w[c][k]) * q.g[c][k];
+    }
+  } else if (by_value) {
+    MOE_EACH(c, k) {
+      const float x = q.x[c][k], da = __fmul_rn(q.dy[c][k], q.g[c][k]);
+      q.dres[c][k] = __fadd_rn(q.dres[c][k], __fmul_rn(rt, fmaf(-x, m, __fmul_rn(da, st.w[c][k]))));
+      st.dw[c][k] = fmaf(da * rt, x, st.dw[c][k]);
+      const float gg = q.dy[c][k] * (x * rt * st.w[c][k]);
       st.dg[c][k] += gg;
       q.g[c][k] = gg;
     }
@@ -377,34 +434,34 @@ __global__ void __launch_bounds__(kNormMaxThreads, V * NCH <= 2 ? 3 : 0) k_norm_
   griddep_wait();
   griddep_launch();
   constexpr bool KEEP = V * NCH <= 16;
-  BwdState<V, NCH, KEEP> st(a);
-  auto load = [&](int64_t t, BwdRow<V, NCH> &q, float &gt) {
+  BwdState<V, NCH, KEEP, false> st(a);
+  auto load = [&](int64_t t, BwdRow<V, NCH> &q, float2 &gt) {
     fill<V, NCH>(q.x, 0.f), fill<V, NCH>(q.dy, 0.f), fill<V, NCH>(q.dres, 0.f), fill<V, NCH>(q.g, 0.f);
     if (t >= a.n) return;
     load_row<V, NCH>(a.x, t * a.x_ld, a.x_bf16, d, q.x);
     load_row<V, NCH>(a.dy, t * a.dy_ld, a.dy_bf16, d, q.dy);
     if (a.dres) load_row<V, NCH>(a.dres, t * a.dres_ld, a.dres_bf16, d, q.dres);
     if (a.gate_kind == MOE_GATE_FULL) load_row<V, NCH>(a.gate, t * a.gate_ld, a.gate_bf16, d, q.g);
-    gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+    gt = token_gates(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
   };
   if (NEXT) {
     BwdRow<V, NCH> q0, q1;
-    float g0 = 1.f, g1 = 1.f;
+    float2 g0{}, g1{};
     load(blockIdx.x, q0, g0);
     for (int64_t t = blockIdx.x; t < a.n; t += 2 * gridDim.x) {
       load(t + gridDim.x, q1, g1);
-      bwd_row<V, NCH, KEEP>(a, t, q0, st, g0, red, threads);
+      bwd_row(a, t, q0, st, g0, red, threads);
       if (t + gridDim.x >= a.n) break;
       load(t + 2 * gridDim.x, q0, g0);
-      bwd_row<V, NCH, KEEP>(a, t + gridDim.x, q1, st, g1, red + 24, threads);
+      bwd_row(a, t + gridDim.x, q1, st, g1, red + 24, threads);
     }
   } else {
     int k = 0;
     for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x, k ^= 1) {
       BwdRow<V, NCH> q;
-      float gt = 1.f;
+      float2 gt{};
       load(t, q, gt);
-      bwd_row<V, NCH, KEEP>(a, t, q, st, gt, red + 24 * k, threads);
+      bwd_row(a, t, q, st, gt, red + 24 * k, threads);
     }
   }
   st.finish(a);
@@ -570,12 +627,12 @@ __global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 2 : 1) k_norm_bwd_rin
     return;
   }
   constexpr bool KEEP = NCH == 1;
-  BwdState<V, NCH, KEEP> st(a);
+  BwdState<V, NCH, KEEP, true> st(a);
   int s = 0, phase = 0, turn = 0;
   for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x, turn ^= 1) {
     BwdRow<V, NCH> q;
     fill<V, NCH>(q.x, 0.f), fill<V, NCH>(q.dy, 0.f), fill<V, NCH>(q.dres, 0.f), fill<V, NCH>(q.g, 0.f);
-    const float gt = token_gate(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
+    const float2 gt = token_gates(a.gate, a.gate_kind, a.gate_act, t * a.gate_ld, a.gate_bf16);
     const unsigned char *p = ring.wait(r, s, phase);
     load_row<V, NCH>(p, 0, a.x_bf16, d, q.x);
     p += d * (a.x_bf16 ? 2 : 4);
@@ -588,7 +645,7 @@ __global__ void __launch_bounds__(kRingThreads, NCH == 1 ? 2 : 1) k_norm_bwd_rin
     if (a.gate_kind == MOE_GATE_FULL) load_row<V, NCH>(p, 0, a.gate_bf16, d, q.g);
     ring.release(s);
     if (++s == r.stages) s = 0, phase ^= 1;
-    bwd_row<V, NCH, KEEP>(a, t, q, st, gt, red + 24 * turn, ring.threads);
+    bwd_row(a, t, q, st, gt, red + 24 * turn, ring.threads);
   }
   st.finish(a);
 }

@@ -246,3 +246,45 @@ def test_graph_and_stream(P):
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("n,d", [(5, 77), (9, 1000), (1, 8), (2000, 264), (2500, 4096), (700, 5000)])
+def test_gradient_of_a_saturated_gate(P, gate, n, d):
+    """Gates from -40 to 40: the slope sigmoid(g) sigmoid(-g) down to 4e-18, to the same relative error as others.
+    (An exponential of z = 40 from the rounded product z log2 e, below 64: half a step, 2^-19, and the constant's
+    own 2^-25 of 58, together 2^-18.2, times log 2: 2^-18.7, inside R.NORM for a single factor.)"""
+    o, dres = randn(n, d, seed=1, std=0.5), randn(n, d, seed=2, std=0.1)
+    w, g = randn(d, seed=3, std=0.3, mean=1.0), gate_of(gate, n, d, F)
+    values = torch.tensor([-40.0, -20.0, -10.0, -1.0, 0.0, 1.0, 10.0, 16.0, 17.0, 20.0, 40.0], device="cuda")
+    flat = g.view(-1)
+    flat.copy_(values[torch.arange(flat.numel(), device="cuda") % len(values)])
+    for post in (w, None):
+        got = P.norm_out_backward(o, dres, weight=post, eps=R.EPS, gate=g, gate_act="sigmoid", scale=0.7)
+        ref = R.norm_out_backward(o, dres, post, g, "sigmoid", 0.7)
+        # the reference's 1 - a in 64 bits has 2^-53 of 1 against a slope of 4e-18: taken as sigmoid(-g)
+        s = torch.sigmoid(g.double())
+        dz = 0.7 * dres.double()
+        u = R.post(o, post)
+        t = dz * u * (s * torch.sigmoid(-g.double()))
+        size = t.abs()
+        if gate == "channel":
+            t, size = t.sum(0), size.sum(0)
+        elif gate == "token":
+            t, size = t.sum(1, keepdim=True), size.sum(1, keepdim=True)
+        R.near(got[2], t, size * 2 * R.NORM + t.abs() * R.HALF[F], "d_gate")
+        for v, name in zip(got[:2], ("d_o", "d_w")):
+            if v is not None:
+                r, size = ref[name]
+                R.near(v, r, size * 2 * R.NORM + r.abs() * R.HALF[F], name)
+
+
+def test_gates_at_the_ends(P):
+    """Gates of +-infinity: weight 1 or 0, slope 0; NaN stays in its own place."""
+    o, dres = randn(6, 64, seed=1), randn(6, 64, seed=2)
+    g = torch.zeros(6, 64, device="cuda")
+    g[0], g[1], g[2], g[3], g[4, 5] = float("inf"), -float("inf"), 200.0, -200.0, float("nan")
+    do, _, dg = P.norm_out_backward(o, dres, gate=g, gate_act="sigmoid")
+    assert torch.equal(do[0], dres[0]) and torch.equal(do[2], dres[2]) and (do[1] == 0).all() and (do[3] == 0).all()
+    assert (dg[:4] == 0).all()
+    assert torch.isnan(do[4, 5]) and torch.isnan(dg[4, 5]) and torch.isnan(do).sum() == 1 and torch.isnan(dg).sum() == 1
