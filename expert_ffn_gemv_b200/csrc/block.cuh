@@ -73,9 +73,11 @@ inline cudaError_t current_sm_count(int *nsm) {
   return cudaSuccess;
 }
 
-// 1 / (1 + exp(-z)) by the approximate power and reciprocal, 3 units in the last place off (from z = -88 on
-// down more, to 0; 1 / inf = 0).  Four instructions: an IEEE division takes ten, an exponential that keeps
-// subnormals three more.
+// 1 / (1 + exp(-z)) by the approximate power and reciprocal.  Relative error: the power's argument is the
+// rounded z log2 e, so that exp(-z) is off by up to 1.25 |z| 2^-24 and the instruction's 2^-22; the reciprocal's
+// 2^-23 and the sum's 2^-24 come on top: (1.25 |z| + 7) 2^-24 for negative z, less for
+// positive z, where exp(-z) counts little.  Below z = -87 it falls to 0 (1 / inf = 0).  Four instructions: an
+// IEEE division takes ten, an exponential that keeps subnormals three more.
 __device__ __forceinline__ float fast_sigmoid(float z, float &e) {  // e: exp(-z)
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));

@@ -288,3 +288,19 @@ def test_gates_at_the_ends(P):
     assert torch.equal(do[0], dres[0]) and torch.equal(do[2], dres[2]) and (do[1] == 0).all() and (do[3] == 0).all()
     assert (dg[:4] == 0).all()
     assert torch.isnan(do[4, 5]) and torch.isnan(dg[4, 5]) and torch.isnan(do).sum() == 1 and torch.isnan(dg).sum() == 1
+
+
+@pytest.mark.parametrize("kind", ["channel", "full"])
+def test_sigmoid_of_gates_by_the_value(P, kind):
+    """o = 1 and a residual of 0 leave the gate's sigmoid alone.  Its exponential has the argument z log2 e rounded
+    (2^-24 of it) with a constant that is 2^-26 off, so an error of 1.25 |z| 2^-24, and is itself good to 2^-22; a
+    reciprocal good to 2^-23 and the rounding of 1 + e follow: (1.25 |z| + 7) 2^-24."""
+    n, d = (1, 4096) if kind == "channel" else (16, 4096)
+    g = torch.rand(n, d, generator=torch.Generator().manual_seed(1), dtype=torch.float64).mul(100).sub(80).float().cuda()
+    one, zero = torch.ones(n, d, device="cuda"), torch.zeros(n, d, device="cuda")
+    gate = g.reshape(-1) if kind == "channel" else g
+    ref = torch.sigmoid(g.double())
+    tol = ref * (1.25 * g.double().abs() + 7) * 2.0 ** -24
+    R.near(P.norm_out(one, zero, gate=gate, gate_act="sigmoid"), ref, tol, "forward")
+    # the gradient's factor: the same, or 1 minus the other one (half a step more)
+    R.near(P.norm_out_backward(one, one, gate=gate, gate_act="sigmoid")[0], ref, tol + ref * 2.0 ** -24, "backward")
