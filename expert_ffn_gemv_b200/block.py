@@ -10,11 +10,11 @@ from __future__ import annotations
 import ctypes as C
 import importlib.util
 from dataclasses import dataclass
-from pathlib import Path
 
 import torch
 
 import expert_ffn_gemv_b200 as P
+from expert_ffn_gemv_b200 import build
 
 TYPES = {P.MOE_F32: torch.float32, P.MOE_BF16: torch.bfloat16}
 CODES = {v: k for k, v in TYPES.items()}
@@ -22,11 +22,15 @@ _ACTS = {"linear": P.MOE_GATE_LINEAR, "sigmoid": P.MOE_GATE_SIGMOID}
 _lib = P.lib()
 
 
-def _load_ext():
-    """The binding (csrc/bind.cpp), bound to the loaded library; raises if it was not built."""
-    path = Path(__file__).resolve().parent / "_lib" / "_block_ext.so"
+def _load_ext(path=build.EXT):
+    """The binding (csrc/bind.cpp), bound to the loaded library; raises if it was not built, or not for the torch
+    and Python that run."""
     if not path.exists():
         raise RuntimeError(f"{path} is missing: build it with `python -m expert_ffn_gemv_b200.build`")
+    was, target = build.ext_built_for(path), build.ext_target()
+    if was != target:
+        raise RuntimeError(f"{path} was built for {was}, not for {target}: build it again with "
+                           "`python -m expert_ffn_gemv_b200.build`")
     spec = importlib.util.spec_from_file_location("_block_ext", path)
     ext = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ext)

@@ -1,11 +1,13 @@
-"""Build the sm_100a shared library libmoe_b200.so in-tree (nvcc, no JIT cache), and the host-side
-binding of its block operators for torch tensors, _block_ext.so (g++).
+"""Build the sm_100a shared library libmoe_b200.so in-tree (nvcc, no JIT cache), and, where PyTorch is
+installed, the host-side binding of the block operators for its tensors, _block_ext.so (g++).
 
     python -m expert_ffn_gemv_b200.build        # or: import expert_ffn_gemv_b200.build as b; b.build()
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -28,8 +30,23 @@ EXT = OUT_DIR / "_block_ext.so"
 EXT_SOURCES = [CSRC / "bind.cpp", ROOT / "include" / "moe.h"]
 
 
+def ext_target() -> str:
+    """What a binding has to be built against to be loaded here."""
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def ext_built_for(path: Path) -> str | None:
+    """What a binding was built against (bind.cpp keeps it as text), None where it does not say."""
+    m = re.search(rb"moe-block-ext-for:([^\0]*)\0", path.read_bytes())
+    return m.group(1).decode() if m else None
+
+
 def build_ext(force: bool = False) -> Path:
-    if not force and EXT.exists() and all(p.stat().st_mtime <= EXT.stat().st_mtime for p in EXT_SOURCES):
+    target = ext_target()
+    if not force and EXT.exists() and all(p.stat().st_mtime <= EXT.stat().st_mtime for p in EXT_SOURCES) \
+            and ext_built_for(EXT) == target:
         return EXT
     import sysconfig
 
@@ -43,7 +60,7 @@ def build_ext(force: bool = False) -> Path:
     libs = Path(torch.__file__).parent / "lib"
     tmp = EXT.with_suffix(f".{os.getpid()}.tmp")
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DMOE_EXT_TARGET="{target}"',
            *[f"-I{i}" for i in inc], str(CSRC / "bind.cpp"), "-o", str(tmp),
            f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -70,10 +87,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: Path | No
     """Compile every .cu into one shared library; `defines` (e.g. ["MOE_DECODE_STAGES=2"]) and
     `out` build a variant elsewhere."""
     lib = LIB if out is None else Path(out)
-    if out is None:
-        build_ext(force)
     if not force and not defines and out is None and not _stale():
-        return LIB
+        return _with_ext(lib, force)
     OUT_DIR.mkdir(exist_ok=True)
     tag = "" if out is None else "_" + lib.stem
     objs = []
@@ -100,6 +115,13 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: Path | No
     os.replace(tmp, lib)
     for o in objs:
         o.unlink(missing_ok=True)
+    return lib if out is not None else _with_ext(lib, force)
+
+
+def _with_ext(lib: Path, force: bool) -> Path:
+    """The library needs nvcc alone: without PyTorch there is nothing to bind to."""
+    if importlib.util.find_spec("torch") is not None:
+        build_ext(force)
     return lib
 
 

@@ -520,6 +520,9 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          METHOD(norm_in), METHOD(norm_out), METHOD(norm_in_backward), METHOD(norm_out_backward),
                          METHOD(adapters_apply), METHOD(ffn_forward), METHOD(ffn_backward),
                          {nullptr, nullptr, 0, nullptr}};
+// Read from the file before it is loaded: a binding of another torch or Python is not.
+__attribute__((used)) const char built_for[] = "moe-block-ext-for:" MOE_EXT_TARGET;
+
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_ext", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
