@@ -3,7 +3,9 @@ adapters of many requests, and the dense gated feed-forward block.
 
 Argument checks and marshalling only.  Tensors are CUDA tensors of one device, matrices 2-D with unit
 stride in their last dimension (rows may be strided); the work goes to that device's current stream.
-Bad tensors raise ``ValueError``, a status other than ok raises ``MoeError``.
+Bad tensors raise ``ValueError``, a status other than ok raises ``MoeError``.  Nothing here is recorded for
+autograd, so that tensors that require grad are refused outside ``torch.no_grad()``: the gradients of the norms
+and the dense block come from the ``_backward`` functions, the adapters have none.
 """
 from __future__ import annotations
 
@@ -60,8 +62,14 @@ def _act(gate_act):
     return _ACTS[gate_act]
 
 
+def _no_grad(t, name):
+    if t.requires_grad and torch.is_grad_enabled():
+        _bad(name, "requires grad, but the call leaves nothing for autograd: make it under torch.no_grad()")
+
+
 def matrix(t, name, dev, shape, dtype=None, dense=False):
     """Checks a 2-D tensor (None in `shape`: any size, but not 0) and returns its row stride."""
+    _no_grad(t, name)
     if t.dim() != 2 or (shape[0] is not None and t.shape[0] != shape[0]) or (shape[1] is not None and t.shape[1] != shape[1]):
         _bad(name, f"shape {tuple(t.shape)}, expected {shape}")
     if t.numel() == 0:
@@ -78,6 +86,7 @@ def matrix(t, name, dev, shape, dtype=None, dense=False):
 
 
 def vector(t, name, dev, n, dtype=None):
+    _no_grad(t, name)
     if t.dim() != 1 or t.shape[0] != n:
         _bad(name, f"shape {tuple(t.shape)}, expected ({n},)")
     if t.device != dev:

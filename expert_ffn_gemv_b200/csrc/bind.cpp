@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -69,7 +70,11 @@ std::string str(const Tensor &t) {
 
 const Tensor &tensor(PyObject *o, const char *name) {
   if (!THPVariable_Check(o)) refuse(name, "is not a tensor");
-  return THPVariable_Unpack(o);
+  const Tensor &t = THPVariable_Unpack(o);
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(name, "requires grad, but the call leaves nothing for autograd: make it under torch.no_grad() and take the "
+                 "gradients from the _backward functions");
+  return t;
 }
 bool given(PyObject *o) { return o != Py_None; }
 

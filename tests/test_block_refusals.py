@@ -178,3 +178,36 @@ def differences(loss, v, grads):
             down[k].reshape(-1)[i] -= e
             got[i] = (loss(up) - loss(down)) / (2 * e)
         assert torch.allclose(got.reshape(v[k].shape), g, rtol=1e-7, atol=1e-7), k
+
+
+def test_wrappers_refuse_tensors_that_require_grad(P):
+    """Nothing is recorded for autograd: without a word a graph through them would train nothing.  (Host tensors:
+    under no_grad the same calls get as far as their device.)"""
+    from expert_ffn_gemv_b200 import block
+
+    def x(grad):
+        return torch.zeros(2, 64, requires_grad=grad)
+
+    def w(grad):
+        return torch.zeros(64, requires_grad=grad)
+
+    def m(grad):
+        return torch.zeros(64, 64, dtype=torch.bfloat16, requires_grad=grad)
+
+    calls = {
+        "x": [lambda g: P.norm_in(x(g), w(False)), lambda g: P.norm_in_backward(x(g), w(False), x(False)), lambda g: P.ffn_forward(m(g), m(False), m(False), m(False))],
+        "weight": [lambda g: P.norm_in(x(False), w(g))],
+        "o": [lambda g: P.norm_out(x(g), x(False)), lambda g: P.norm_out_backward(x(g), x(False))],
+        "residual": [lambda g: P.norm_out(x(False), x(g))],
+        "w_up": [lambda g: P.ffn_forward(m(False), m(False), m(g), m(False)), lambda g: P.ffn_backward(m(False), m(False), m(False), m(g), m(False), (m(False), m(False)))],
+        "x_in": [lambda g: block.matrix(x(g), "x_in", torch.device("cuda", 0), (None, 64))],
+        "norm_in": [lambda g: block.vector(w(g), "norm_in", torch.device("cuda", 0), 64)],
+    }
+    for name, some in calls.items():
+        for call in some:
+            with pytest.raises(ValueError, match=f"^{name}: requires grad"):
+                call(True)
+            with torch.no_grad(), pytest.raises(ValueError, match="cuda|CUDA"):
+                call(True)
+            with pytest.raises(ValueError, match="cuda|CUDA"):
+                call(False)

@@ -304,3 +304,15 @@ def test_sigmoid_of_gates_by_the_value(P, kind):
     R.near(P.norm_out(one, zero, gate=gate, gate_act="sigmoid"), ref, tol, "forward")
     # the gradient's factor: the same, or 1 minus the other one (half a step more)
     R.near(P.norm_out_backward(one, one, gate=gate, gate_act="sigmoid")[0], ref, tol + ref * 2.0 ** -24, "backward")
+
+
+def test_parameters_under_no_grad(P):
+    x, w, g = randn(3, 64, seed=1), randn(64, seed=2), randn(3, 64, seed=3)
+    want = P.norm_out(x, x, weight=w, gate=g)
+    p, q, r = (torch.nn.Parameter(t.clone()) for t in (x, w, g))
+    for bad in ((p, x, w, g), (x, p, w, g), (x, x, q, g), (x, x, w, r)):
+        with pytest.raises(ValueError, match="requires grad"):
+            P.norm_out(bad[0], bad[1], weight=bad[2], gate=bad[3])
+    with torch.no_grad():
+        got = P.norm_out(p, p, weight=q, gate=r)
+    assert torch.equal(got, want) and not got.requires_grad
