@@ -919,10 +919,13 @@ moe_status moe_adapters_load(moe_adapters *h, int32_t slot, const void *a, const
     const int64_t r16 = round16(rank);
     const int blocks_a = static_cast<int>((r16 * ((g.d_in + 31) / 32 * 32) + 255) / 256);
     const int blocks_b = static_cast<int>((r16 * ((g.d_out + 31) / 32 * 32) + 255) / 256);
-    k_adapter_pack<<<rank ? blocks_a + blocks_b : 1, 256, 0, st>>>(
-        static_cast<const __nv_bfloat16 *>(src[0]), static_cast<const __nv_bfloat16 *>(src[1]), h->a + h->a_slot * slot,
-        h->b + h->b_slot * slot, h->meta + slot, AdMeta{rank, scale}, g.d_in, g.d_out, blocks_a);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(rank ? blocks_a + blocks_b : 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    e = cudaLaunchKernelEx(&cfg, k_adapter_pack, static_cast<const __nv_bfloat16 *>(src[0]),
+                           static_cast<const __nv_bfloat16 *>(src[1]), h->a + h->a_slot * slot, h->b + h->b_slot * slot,
+                           h->meta + slot, AdMeta{rank, scale}, g.d_in, g.d_out, blocks_a);
   }
   if (e == cudaSuccess && host) e = cudaStreamSynchronize(st);
   return e == cudaSuccess ? MOE_OK : ad_cuda(h, e, "adapter load");

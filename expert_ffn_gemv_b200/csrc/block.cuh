@@ -54,6 +54,13 @@ __device__ __forceinline__ void hold_back(uint64_t clocks) {
   }
 }
 
+// The status of a call whose own CUDA call returned e; an error is not left for whoever asks next.
+inline moe_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SMs of the current device (asked once per device).

@@ -1059,14 +1059,10 @@ moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
     s.y = p->y, s.y_ld = p->y_stride, s.y_bf16 = p->y_dtype == MOE_BF16;
     s.h = h, s.g = static_cast<float *>(p->save_gate), s.u = static_cast<float *>(p->save_up);
     s.n = n, s.d = d, s.f = f;
-    e = launch_small(s, st);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return cuda_status(launch_small(s, st));
   }
   FfnDevice dev{};
-  if ((e = ffn_setup(&dev)) != cudaSuccess) {
-    cudaGetLastError();
-    return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
-  }
+  if ((e = ffn_setup(&dev)) != cudaSuccess) return cuda_status(e);
   GemmArgs a{};
   {
     Maps m{dev.encode, a};
@@ -1078,7 +1074,7 @@ moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
     a.f_ld = f, a.err = err;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
-  if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((e = launch_gemm<kEpiSwiglu>(a, dev, st)) != cudaSuccess) return cuda_status(e);
   GemmArgs b{};
   {
     Maps m{dev.encode, b};
@@ -1090,8 +1086,7 @@ moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
     b.err = err;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
   }
-  e = launch_gemm<kEpiPlain>(b, dev, st);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cuda_status(launch_gemm<kEpiPlain>(b, dev, st));
 }
 }  // namespace moe
 
@@ -1111,10 +1106,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   FfnDevice dev{};
   cudaError_t e;
-  if ((e = ffn_setup(&dev)) != cudaSuccess) {
-    cudaGetLastError();
-    return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
-  }
+  if ((e = ffn_setup(&dev)) != cudaSuccess) return cuda_status(e);
   const uint64_t nf = align_ws(static_cast<uint64_t>(n) * f * 2) / 2;
   __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(p->workspace), *dg = h + nf, *du = dg + nf;
   {
@@ -1126,7 +1118,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     a.g = static_cast<float *>(const_cast<void *>(p->save_gate)), a.u = static_cast<float *>(const_cast<void *>(p->save_up));
     a.h = h, a.dg = dg, a.du = du, a.f_ld = f;
     if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-    if ((e = launch_gemm<kEpiDswiglu>(a, dev, st)) != cudaSuccess) return MOE_ERR_CUDA;
+    if ((e = launch_gemm<kEpiDswiglu>(a, dev, st)) != cudaSuccess) return cuda_status(e);
   }
   // everything else in one launch: dx (its tiles run over both matrices), then the weights' gradients; few
   // tokens: dx before them
@@ -1141,7 +1133,7 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     const bool apart = dx_apart(n, d, f, dev);
     if (apart || (!p->dw_gate && !p->dw_down)) {
       if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-      if (launch_gemm<kEpiPlain>(a, dev, st, apart) != cudaSuccess) return MOE_ERR_CUDA;
+      if ((e = launch_gemm<kEpiPlain>(a, dev, st, apart)) != cudaSuccess) return cuda_status(e);
       a.n_prob = m.n = 0;
     }
   }
@@ -1160,17 +1152,13 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_bwd_args *p, void *stream) 
     q.out = p->dw_down, q.ld = f, q.out_bf16 = 1;
   }
   if (!m.ok) return MOE_ERR_INVALID_ARGUMENT;
-  if (a.n_prob && launch_gemm<kEpiPlain>(a, dev, st, false) != cudaSuccess) return MOE_ERR_CUDA;
-  return MOE_OK;
+  return cuda_status(a.n_prob ? launch_gemm<kEpiPlain>(a, dev, st, false) : cudaSuccess);
 }
 
 extern "C" moe_status moe_block_check(void) {
   BlockWord w;
   cudaError_t e = cudaDeviceSynchronize();  // every stream of the device, also those that no other waits for
   if (e == cudaSuccess) e = block_word(&w);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
+  if (e != cudaSuccess) return cuda_status(e);
   return __atomic_exchange_n(w.host, 0u, __ATOMIC_ACQ_REL) ? MOE_ERR_TIMEOUT : MOE_OK;
 }

@@ -701,11 +701,10 @@ int norm_threads(int d, int v) {
   return t < kNormMaxThreads ? t : kNormMaxThreads;
 }
 
-// Calls f with the instantiation that holds a row of d <= kNormMaxD values, v at a time.
 // Launch with programmatic stream serialization: a kernel may begin while the one before it ends, and
 // waits for its results itself.
 template <typename... P>
-void launch(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, const P &...args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, const P &...args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -716,24 +715,22 @@ void launch(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);  // an error is the last error, which the callers read
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Calls f with the instantiation that holds a row of d <= kNormMaxD values, v at a time.
 template <typename F>
 cudaError_t pick_norm(int d, int v, F f) {
   const int threads = norm_threads(d, v), nch = (d + v * threads - 1) / (v * threads);
 #define MOE_NORM_CASE(V, N) f(std::integral_constant<int, V>{}, std::integral_constant<int, N>{}, threads)
-  if (v == 8)
-    nch <= 1 ? MOE_NORM_CASE(8, 1) : nch <= 2 ? MOE_NORM_CASE(8, 2) : MOE_NORM_CASE(8, 4);
-  else if (v == 4)
-    nch <= 1 ? MOE_NORM_CASE(4, 1) : nch <= 2 ? MOE_NORM_CASE(4, 2) : nch <= 4 ? MOE_NORM_CASE(4, 4) : MOE_NORM_CASE(4, 8);
-  else if (v == 2)
-    nch <= 2 ? MOE_NORM_CASE(2, 2) : nch <= 4 ? MOE_NORM_CASE(2, 4) : nch <= 8 ? MOE_NORM_CASE(2, 8) : MOE_NORM_CASE(2, 16);
-  else
-    nch <= 2 ? MOE_NORM_CASE(1, 2) : nch <= 4 ? MOE_NORM_CASE(1, 4) : nch <= 8 ? MOE_NORM_CASE(1, 8)
-                                   : nch <= 16 ? MOE_NORM_CASE(1, 16) : MOE_NORM_CASE(1, 32);
+  if (v == 8) return nch <= 1 ? MOE_NORM_CASE(8, 1) : nch <= 2 ? MOE_NORM_CASE(8, 2) : MOE_NORM_CASE(8, 4);
+  if (v == 4)
+    return nch <= 1 ? MOE_NORM_CASE(4, 1) : nch <= 2 ? MOE_NORM_CASE(4, 2) : nch <= 4 ? MOE_NORM_CASE(4, 4) : MOE_NORM_CASE(4, 8);
+  if (v == 2)
+    return nch <= 2 ? MOE_NORM_CASE(2, 2) : nch <= 4 ? MOE_NORM_CASE(2, 4) : nch <= 8 ? MOE_NORM_CASE(2, 8) : MOE_NORM_CASE(2, 16);
+  return nch <= 2 ? MOE_NORM_CASE(1, 2) : nch <= 4 ? MOE_NORM_CASE(1, 4) : nch <= 8 ? MOE_NORM_CASE(1, 8)
+                                        : nch <= 16 ? MOE_NORM_CASE(1, 16) : MOE_NORM_CASE(1, 32);
 #undef MOE_NORM_CASE
-  return cudaGetLastError();
 }
 
 bool bad_dtype(int dt) { return dt != MOE_F32 && dt != MOE_BF16; }
@@ -797,13 +794,10 @@ struct RingPlan {
 template <int MOST, typename F>
 cudaError_t pick_ring(int d, F f) {
   const int nch = (d + 8 * kNormMaxThreads - 1) / (8 * kNormMaxThreads);
-  if (nch <= 1)
-    f(std::integral_constant<int, 1>{});
-  else if (nch <= 2)
-    f(std::integral_constant<int, 2>{});
-  else if constexpr (MOST == 4)
-    f(std::integral_constant<int, 4>{});
-  return cudaGetLastError();
+  if (nch <= 1) return f(std::integral_constant<int, 1>{});
+  if constexpr (MOST == 4)
+    if (nch > 2) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 2>{});
 }
 
 // Once per device, with it current.
@@ -829,13 +823,13 @@ moe_status launch_fwd(const NormFwd &a, int n, int v, cudaStream_t st, uint32_t 
   if (e == cudaSuccess && p.r.stages) {
     e = configure_rings();
     if (e == cudaSuccess)
-      e = pick_ring<4>(a.d, [&](auto nch) { launch(k_norm_fwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, a, p.r, n); });
+      e = pick_ring<4>(a.d, [&](auto nch) { return launch(k_norm_fwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, a, p.r, n); });
   } else if (e == cudaSuccess) {
     e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
-      launch(k_norm_fwd<decltype(vv)::value, decltype(nch)::value>, n, threads, 0, st, a);
+      return launch(k_norm_fwd<decltype(vv)::value, decltype(nch)::value>, n, threads, 0, st, a);
     });
   }
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cuda_status(e);
 }
 
 // Blocks of the backward grid: enough to fill the device, no more than rows; the partial sums need
@@ -854,7 +848,9 @@ moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf
   const RingPlan p({{a.x, a.x_ld, a.x_bf16}, {a.dy, a.dy_ld, a.dy_bf16}, {a.dres, a.dres_ld, a.dres_bf16},
                     {full ? a.gate : nullptr, a.gate_ld, a.gate_bf16}}, a.n, a.d, v, true, nullptr);
   int blocks = p.blocks;
-  if (p.err != cudaSuccess || (!p.r.stages && bwd_blocks(a.n, &blocks) != cudaSuccess)) return MOE_ERR_CUDA;
+  cudaError_t e = p.err;
+  if (e == cudaSuccess && !p.r.stages) e = bwd_blocks(a.n, &blocks);
+  if (e != cudaSuccess) return cuda_status(e);
   const int sums = (dw ? 1 : 0) + (dg ? 1 : 0);
   if (sums && (!ws || ws_bytes < moe_norm_workspace(a.n, a.d) || !aligned16(ws))) return MOE_ERR_INVALID_ARGUMENT;
   float *part = static_cast<float *>(ws);
@@ -871,21 +867,17 @@ moe_status run_bwd(NormBwd &a, int v, void *dw, int dw_bf16, void *dg, int dg_bf
     a.dg_part = part;
     c.part[k] = part, c.out[k] = dg, c.bf16[k] = dg_bf16, ++k;
   }
-  cudaError_t e;
   if (p.r.stages) {
     e = configure_rings();
     if (e == cudaSuccess)
-      e = pick_ring<2>(a.d, [&](auto nch) { launch(k_norm_bwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, static_cast<const NormBwd &>(a), p.r); });
+      e = pick_ring<2>(a.d, [&](auto nch) { return launch(k_norm_bwd_ring<decltype(nch)::value>, p.blocks, p.threads + 32, p.smem, st, static_cast<const NormBwd &>(a), p.r); });
   } else {
     e = pick_norm(a.d, v, [&](auto vv, auto nch, int threads) {
-      launch(k_norm_bwd<decltype(vv)::value, decltype(nch)::value>, blocks, threads, 0, st, static_cast<const NormBwd &>(a));
+      return launch(k_norm_bwd<decltype(vv)::value, decltype(nch)::value>, blocks, threads, 0, st, static_cast<const NormBwd &>(a));
     });
   }
-  if (e == cudaSuccess && sums) {
-    launch(k_colsum, dim3((a.d + 31) / 32, sums), dim3(32, 32), 0, st, c);
-    e = cudaGetLastError();
-  }
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (e == cudaSuccess && sums) e = launch(k_colsum, dim3((a.d + 31) / 32, sums), dim3(32, 32), 0, st, c);
+  return cuda_status(e);
 }
 
 }  // namespace
