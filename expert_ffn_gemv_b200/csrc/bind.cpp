@@ -103,20 +103,27 @@ void weights(const Tensor &t, const char *name, c10::Device dev, int64_t n) {
   vector(t, name, dev, n, code(t) == MOE_BF16 ? at::kBFloat16 : at::kFloat);
 }
 
-// The bytes a tensor spans.
+// The bytes a tensor spans: rows of `width` bytes, `pitch` apart (0: one row).
 struct Span {
-  uintptr_t lo, hi;
+  uintptr_t lo, hi, width, pitch;
   explicit Span(const Tensor &t) {
-    int64_t last = 0;
-    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    const int64_t size = t.element_size(), rows = t.dim() == 2 ? t.size(0) : 1;
     lo = reinterpret_cast<uintptr_t>(t.data_ptr());
-    hi = lo + (last + 1) * t.element_size();
+    width = t.size(-1) * size;
+    pitch = rows > 1 ? t.stride(0) * size : 0;
+    hi = lo + (rows - 1) * pitch + width;
+  }
+  // Rows between the other one's, as of two column ranges of one matrix.
+  bool beside(const Span &b) const {
+    if (!pitch || pitch != b.pitch) return false;
+    const uintptr_t at = b.lo >= lo ? (b.lo - lo) % pitch : (pitch - (lo - b.lo) % pitch) % pitch;
+    return at >= width && at + b.width <= pitch;
   }
 };
 // An output shares no memory with an input, unless `may` and it is that input: same start, strides, type.
 void apart(const Tensor &out, const char *name, const Tensor &in, bool may = false) {
   const Span a(out), b(in);
-  if (a.lo >= b.hi || b.lo >= a.hi) return;
+  if (a.lo >= b.hi || b.lo >= a.hi || a.beside(b)) return;
   if (may && a.lo == b.lo && out.strides() == in.strides() && out.scalar_type() == in.scalar_type()) return;
   refuse(name, "overlaps another tensor of the call");
 }

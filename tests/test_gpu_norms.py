@@ -316,3 +316,27 @@ def test_parameters_under_no_grad(P):
     with torch.no_grad():
         got = P.norm_out(p, p, weight=q, gate=r)
     assert torch.equal(got, want) and not got.requires_grad
+
+
+@pytest.mark.parametrize("n,d", [(5, 64), (3, 77), (2000, 264)])
+def test_column_ranges_of_one_matrix(P, n, d):
+    """Inputs and outputs between each other's rows share no memory; one column more and they do."""
+    o, w = randn(n, d, seed=1), randn(d, seed=3, mean=1.0)
+    both = randn(n, 3 * d + 2, seed=2)
+    keep = both.clone()
+    res, new, h = both[:, :d], both[:, d:2 * d], both[:, 2 * d + 1:3 * d + 1]
+    # (rows off a 16-byte boundary are summed in another order than vectors: each is held to the definition)
+    ref, term = R.norm_out(o, res, w, None, "linear", 1.0)
+    P.norm_out(o, res, weight=w, next_weight=w, out=new, next_out=h)
+    R.near(new, ref, term * R.NORM + ref.abs() * (2.0 ** -23 + R.HALF[F]), "res")
+    ref = R.norm_in(new, w)
+    R.near(h, ref, ref.abs() * (R.NORM + R.HALF[F]), "h")
+    P.norm_in(new, w, out=res)
+    R.near(res, ref, ref.abs() * (R.NORM + R.HALF[F]), "h")
+    assert torch.equal(both[:, 2 * d], keep[:, 2 * d]) and torch.equal(both[:, 3 * d + 1], keep[:, 3 * d + 1])
+    for out in (both[:, 1:d + 1], both[:, d - 1:2 * d - 1], both[:, :d]):
+        with pytest.raises(ValueError, match="overlaps"):
+            P.norm_out(o, both[:, :d], out=both[:, d:2 * d], next_weight=w, next_out=out)
+    with pytest.raises(ValueError, match="overlaps"):
+        P.norm_in(both[1:, :d], w, out=both[:-1, d - 1:2 * d - 1])
+    P.norm_in(both[1:, :d], w, out=both[:-1, d:2 * d])  # of other rows
