@@ -936,6 +936,7 @@ cudaError_t block_word(BlockWord *w) {
 }  // namespace moe
 
 extern "C" moe_status moe_debug_set_ring_spin_limit(uint64_t cycles) {
+  if (cycles > kRingSpin / 10) return MOE_ERR_INVALID_ARGUMENT;
   g_ring_limit.store(cycles, std::memory_order_relaxed);
   return MOE_OK;
 }

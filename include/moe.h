@@ -383,7 +383,8 @@ moe_status moe_forward_blocks(moe_handle *h, int32_t first_layer, int32_t n_laye
  * fail allocations that would take the handle above `bytes` (0 = no cap).
  * moe_debug_set_ring_spin_limit: the same limit for the bulk-copy rings of the norms over many rows
  * and of the adapters, process-wide, for the launches that follow; each block's first copies are then held back for four
- * times as long, so that the waits for them run out. */
+ * times as long, so that the waits for them run out
+ * (200 million cycles at most). */
 moe_status moe_debug_set_spin_limit(moe_handle *h, uint64_t cycles);
 moe_status moe_debug_set_alloc_cap(moe_handle *h, uint64_t bytes);
 moe_status moe_debug_set_ring_spin_limit(uint64_t cycles);

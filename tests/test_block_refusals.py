@@ -211,3 +211,10 @@ def test_wrappers_refuse_tensors_that_require_grad(P):
                 call(True)
             with pytest.raises(ValueError, match="cuda|CUDA"):
                 call(False)
+
+
+def test_ring_limit(P):
+    """Copies are held back for four times as long: no longer than half a second."""
+    for cycles in (200_000_001, 1 << 62, (1 << 64) - 1):
+        assert P.moe_debug_set_ring_spin_limit(cycles) == BAD
+    assert P.moe_debug_set_ring_spin_limit(200_000_000) == P.MOE_OK and P.moe_debug_set_ring_spin_limit(0) == P.MOE_OK
