@@ -61,6 +61,12 @@ inline moe_status cuda_status(cudaError_t e) {
   return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
 }
 
+// An output in the place of an input, whose rows or values lie elsewhere: rows would be written before they
+// are read.
+inline bool misplaced(const void *out, int64_t out_ld, int out_dt, const void *in, int64_t in_ld, int in_dt, int n) {
+  return out && out == in && (out_dt != in_dt || (n > 1 && out_ld != in_ld));
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SMs of the current device (asked once per device).

@@ -1043,6 +1043,7 @@ moe_status ffn_forward_run(const moe_ffn_args *p, void *stream, uint32_t *err) {
       bad_act(p->y, p->y_stride, d, n, p->y_dtype == MOE_BF16 ? 2 : 4) ||
       (p->add && ((p->add_dtype != MOE_F32 && p->add_dtype != MOE_BF16) ||
                   bad_act(p->add, p->add_stride, d, n, p->add_dtype == MOE_BF16 ? 2 : 4))) ||
+      misplaced(p->y, p->y_stride, p->y_dtype, p->add, p->add_stride, p->add_dtype, n) ||
       (p->save_gate != nullptr) != (p->save_up != nullptr) || (p->save_gate && (bad_mat(p->save_gate) || bad_mat(p->save_up))) ||
       bad_mat(p->workspace) || p->workspace_bytes < moe_ffn_workspace(n, d, f, 0))
     return MOE_ERR_INVALID_ARGUMENT;

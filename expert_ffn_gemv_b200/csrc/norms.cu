@@ -947,7 +947,7 @@ moe_status norm_in_run(const void *x, int32_t x_dtype, int64_t x_stride, const v
                        void *stream, uint32_t *err) {
   if (n_tokens < 1 || d_model < 1 || !weight || !(eps >= 0.f) || unit_offset < 0 || unit_offset > 1 ||
       bad_rows(x, x_stride, d_model, n_tokens, x_dtype) || bad_rows(h, h_stride, d_model, n_tokens, h_dtype) ||
-      bad_vec(weight, w_dtype))
+      bad_vec(weight, w_dtype) || misplaced(h, h_stride, h_dtype, x, x_stride, x_dtype, n_tokens))
     return MOE_ERR_INVALID_ARGUMENT;
   if (d_model > kNormMaxD) return MOE_ERR_UNSUPPORTED;
   if (const moe_status s = err ? MOE_OK : block_pending()) return s;
@@ -968,7 +968,11 @@ moe_status norm_out_run(const moe_norm_out_args *p, void *stream, uint32_t *err)
       bad_rows(p->residual, p->res_stride, d, n, p->res_dtype) ||
       bad_rows(p->res_out, p->res_out_stride, d, n, p->res_out_dtype) || p->unit_offset < 0 || p->unit_offset > 1 ||
       (p->weight && (bad_vec(p->weight, p->w_dtype) || !(p->eps >= 0.f))) || (p->next_weight != nullptr) != (p->h != nullptr) ||
-      (p->h && (bad_rows(p->h, p->h_stride, d, n, p->h_dtype) || bad_vec(p->next_weight, p->w_dtype) || !(p->next_eps >= 0.f))))
+      (p->h && (bad_rows(p->h, p->h_stride, d, n, p->h_dtype) || bad_vec(p->next_weight, p->w_dtype) || !(p->next_eps >= 0.f))) ||
+      p->h == p->res_out ||
+      misplaced(p->res_out, p->res_out_stride, p->res_out_dtype, p->residual, p->res_stride, p->res_dtype, n) ||
+      misplaced(p->res_out, p->res_out_stride, p->res_out_dtype, p->o, p->o_stride, p->o_dtype, n) ||
+      misplaced(p->h, p->h_stride, p->h_dtype, p->o, p->o_stride, p->o_dtype, n))
     return MOE_ERR_INVALID_ARGUMENT;
   const moe_status gs = check_gate(p->gate, p->gate_kind, p->gate_act, p->gate_dtype, p->gate_stride, d, n);
   if (gs != MOE_OK) return gs;
@@ -1019,7 +1023,8 @@ extern "C" moe_status moe_norm_in_backward(const moe_norm_in_bwd_args *p, void *
   if (n < 1 || d < 1 || bad_rows(p->x, p->x_stride, d, n, p->x_dtype) || bad_rows(p->dh, p->dh_stride, d, n, p->dh_dtype) ||
       bad_rows(p->dx, p->dx_stride, d, n, p->dx_dtype) || !p->weight || bad_vec(p->weight, p->w_dtype) ||
       (p->dres && bad_rows(p->dres, p->dres_stride, d, n, p->dres_dtype)) || (p->dweight && bad_vec(p->dweight, p->w_dtype)) ||
-      p->unit_offset < 0 || p->unit_offset > 1 || !(p->eps >= 0.f))
+      p->unit_offset < 0 || p->unit_offset > 1 || !(p->eps >= 0.f) ||
+      misplaced(p->dx, p->dx_stride, p->dx_dtype, p->dres, p->dres_stride, p->dres_dtype, n))
     return MOE_ERR_INVALID_ARGUMENT;
   if (d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
   if (const moe_status s = block_pending()) return s;

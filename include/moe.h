@@ -200,7 +200,8 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * pins a page of host memory for error words).  Strides count values between the starts of
  * consecutive rows.  Each result is
  * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
- * Outputs may not overlap inputs unless said so.
+ * Outputs may not overlap inputs unless said so; one in an input's place that has another type or
+ * row stride is refused.
  * ------------------------------------------------------------------------------------------- */
 /* A bounded wait of the norms' or the dense block's kernels that ran out makes the next call of one of
  * them on that device, whoever made the first, return MOE_ERR_TIMEOUT, once and with nothing launched:

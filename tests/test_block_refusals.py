@@ -218,3 +218,27 @@ def test_ring_limit(P):
     for cycles in (200_000_001, 1 << 62, (1 << 64) - 1):
         assert P.moe_debug_set_ring_spin_limit(cycles) == BAD
     assert P.moe_debug_set_ring_spin_limit(200_000_000) == P.MOE_OK and P.moe_debug_set_ring_spin_limit(0) == P.MOE_OK
+
+
+def test_outputs_in_an_inputs_place(P):
+    """With another type or row stride than the input's, rows would be written before they are read.  (Pointers of
+    their own everywhere else; d_model 9000 has the sound calls end as unsupported, before any launch.)"""
+    L, d = P.lib(), 9000
+    ld = dict(o_stride=d, res_stride=d, res_out_stride=d, h_stride=d)
+    same = dict(n_tokens=2, d_model=d, o=1 << 20, residual=2 << 20, res_out=3 << 20, next_weight=4 << 20, h=5 << 20, eps=1e-6,
+                next_eps=1e-6, scale=1.0, **ld)
+    for kw, status in [(dict(), UNSUP), (dict(res_out=2 << 20), UNSUP), (dict(res_out=1 << 20), UNSUP), (dict(h=1 << 20), UNSUP),
+                       (dict(res_out=2 << 20, res_out_dtype=1), BAD), (dict(res_out=2 << 20, res_dtype=1), BAD),
+                       (dict(res_out=2 << 20, res_out_stride=d + 8), BAD), (dict(res_out=1 << 20, o_dtype=1), BAD),
+                       (dict(h=1 << 20, h_dtype=1), BAD), (dict(h=1 << 20, h_stride=d + 1), BAD), (dict(h=3 << 20), BAD),
+                       (dict(res_out=2 << 20, res_out_stride=d + 8, n_tokens=1), UNSUP)]:
+        assert L.moe_norm_out(C.byref(P.moe_norm_out_args(**{**same, **kw})), None) == status, kw
+    for x_dt, h_dt, h_ld, status in [(0, 0, d, UNSUP), (0, 1, d, BAD), (1, 0, d, BAD), (0, 0, d + 4, BAD)]:
+        assert L.moe_norm_in(64, x_dt, d, 1 << 20, 0, 1e-6, 0, 64, h_dt, h_ld, 2, d, None) == status
+    same = dict(n_tokens=2, d_model=d, x=64, weight=1 << 20, dh=2 << 20, dres=3 << 20, dx=3 << 20, x_stride=d, dh_stride=d,
+                dres_stride=d, dx_stride=d)
+    for kw, status in [(dict(), UNSUP), (dict(dx_dtype=1), BAD), (dict(dres_stride=d + 1), BAD), (dict(dx=4 << 20, dx_dtype=1), UNSUP)]:
+        assert L.moe_norm_in_backward(C.byref(P.moe_norm_in_bwd_args(**{**same, **kw})), None) == status, kw
+    for kw in (dict(add_dtype=1), dict(y_dtype=1), dict(add_stride=72)):
+        a = P.moe_ffn_args(**{**FFN, **dict(add=1 << 20, y=1 << 20, add_stride=64), **kw})
+        assert L.moe_ffn_forward(C.byref(a), None) == BAD, kw
