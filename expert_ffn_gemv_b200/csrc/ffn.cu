@@ -3,8 +3,10 @@
 //   dh = dy Wd   dg = dh u silu'(g)   du = dh silu(g)
 //   dx = dg Wg + du Wu   dWg = dg^T x   dWu = du^T x   dWd = dy^T h
 // x, dy n x d; Wg, Wu f x d; Wd d x f; all products of bf16 values with fp32 accumulators, each
-// result rounded once.  h, dg and du are operands of the next products and so in bf16: their rounding
-// (2^-9 of a value) is no more than that of the bf16 results.  g and u, from which the backward
+// result rounded once.  h, dg and du are operands of the next products and so in bf16: their rounding (half
+// a step, up to 2^-8 of a value) is of the size of the bf16 results' own and adds to it (forward 2.4e-3 off
+// 64 bits in relative 2-norm, 1.7e-3 with all of them in fp32); a second bf16 part of each would double the
+// products that take them.  g and u, from which the backward
 // computes h, dg and du again, are saved in fp32: in bf16 their rounding would come on top of it
 // (gradients 3.5e-3 off, relative 2-norm, against 2.4e-3).
 //
@@ -53,7 +55,8 @@ struct GemmArgs {
 
 // Threads: sixteen epilogue warps (TMEM lanes 32 (w % 4) .., 32-column chunks w / 4, w / 4 + 4), a TMA
 // producer warp, an MMA warp.  A CTA holds 128 rows of A and up to 128 rows of B per stage: tiles of
-// 128 x 128 for one CTA, of 256 x 256 for a pair (cta_group::2), whose CTAs share their halves of B.
+// 128 x 64 or 128 x 128 for one CTA, of 256 x 128 or 256 x 256 for a pair (cta_group::2), whose CTAs share
+// their halves of B (choose_form).
 // With eight epilogue warps the arithmetic of the gated ones (some 30 instructions a value) took 25 us
 // a tile of 256 x 256, its 2048-deep product 12 us, and the last tile's plain one 4.3 us.
 // Bound by the tensor cores under the power cap: 8,192 x 2,048 x 8,192 forward 596 us, 1,384 TFLOP/s; small

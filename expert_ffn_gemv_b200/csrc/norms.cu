@@ -15,7 +15,7 @@
 // to 2e-5.  With them contracted, one gradient in sixteen over random shapes was further off.
 // Sums over columns are taken over the row's threads (shuffles, then the warps in order), sums over
 // tokens (dw, the gradient of a channel gate) in two steps: every block of a grid that depends on the
-// device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No atomics:
+// sizes and the device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No atomics:
 // the same call gives the same bits.
 #include <math.h>
 #include <string.h>

@@ -198,8 +198,17 @@ moe_status moe_route_noalloc(const void *router_w, int32_t router_dtype, const f
  * enqueue on `stream`, never synchronise the host and allocate nothing, so they can be captured
  * into a CUDA graph (after a first call outside a capture, which loads and configures kernels and
  * pins a page of host memory for error words).  Strides count values between the starts of
- * consecutive rows.  Each result is
- * computed in fp32 and rounded once to its type; calls with the same inputs give the same bits.
+ * consecutive rows.  Calls with the same inputs give the same bits.
+ *
+ * Sums, norms and accumulators are held in fp32 and each result is rounded once to its type.  Three
+ * things inside are held to less than fp32:
+ *   - the dense block's hidden values, and in its backward the gradients of its gate and up products,
+ *     are bf16 between the products, as operands of the tensor cores: half a step is up to 2^-8 of a
+ *     value, and bf16 results are 2.4e-3 off in place of 1.7e-3 (relative 2-norm, against 64 bits);
+ *   - fp32 x and the low-rank values of the adapters enter bf16 products as parts: exactly where out
+ *     is fp32, to 2^-16 of a value where it is bf16;
+ *   - SiLU and the sigmoids of gates by the value (channel, full) use approximate instructions: an
+ *     argument z costs up to (1.25 |z| + 7) 2^-24, relative.  A token's gate takes expf and a division.
  * Outputs may not overlap inputs unless said so; one in an input's place that has another type or
  * row stride is refused.
  * ------------------------------------------------------------------------------------------- */
@@ -317,7 +326,8 @@ uint64_t moe_adapters_device_bytes(const moe_adapters *h);
 
 /* Dense gated feed-forward block, bf16 weights: y = w_down (silu(w_gate x) * (w_up x)) (+ add).
  * n_tokens 1..1048576; d_model and d_ff: multiples of 8, 8..65536; every pointer 16-byte aligned, every row stride a
- * multiple of 16 bytes.  The hidden values are kept in bf16 between the products. */
+ * multiple of 16 bytes.  The hidden values are kept in bf16 between the products (the pre-activations, if
+ * saved, in fp32). */
 typedef struct {
   uint32_t struct_size;
   int32_t n_tokens, d_model, d_ff;
@@ -335,7 +345,8 @@ typedef struct {
 uint64_t moe_ffn_workspace(int32_t n_tokens, int32_t d_model, int32_t d_ff, int32_t backward);
 moe_status moe_ffn_forward(const moe_ffn_args *args, void *stream);
 
-/* Its gradients from dy (of the block alone: the gradient of add is dy itself).  All outputs bf16;
+/* Its gradients from dy (of the block alone: the gradient of add is dy itself).  All outputs bf16; the
+ * gradients of the gate and up products, operands of all of them, are bf16 too, and h is made again in bf16.
  * dx, the pair dw_gate / dw_up and dw_down may each be NULL, not all of them. */
 typedef struct {
   uint32_t struct_size;
