@@ -6,9 +6,9 @@
 // result rounded once.  h, dg and du are operands of the next products and so in bf16: their rounding (half
 // a step, up to 2^-8 of a value) is of the size of the bf16 results' own and adds to it (forward 2.4e-3 off
 // 64 bits in relative 2-norm, 1.7e-3 with all of them in fp32); a second bf16 part of each would double the
-// products that take them.  g and u, from which the backward
-// computes h, dg and du again, are saved in fp32: in bf16 their rounding would come on top of it
-// (gradients 3.5e-3 off, relative 2-norm, against 2.4e-3).
+// products that take them.  g and u, from which the backward computes h, dg and du again, are saved in
+// fp32: in bf16 their rounding would come on top of it (gradients 3.5e-3 off, relative 2-norm, against
+// 2.4e-3).
 //
 // Few tokens: the weights stream once through mma.sync operands (k_ffn_up, k_ffn_down), bound by
 // their bytes.  More tokens: one warp-specialised tcgen05 kernel (k_ffn_gemm) for every product,

@@ -15,8 +15,8 @@
 // to 2e-5.  With them contracted, one gradient in sixteen over random shapes was further off.
 // Sums over columns are taken over the row's threads (shuffles, then the warps in order), sums over
 // tokens (dw, the gradient of a channel gate) in two steps: every block of a grid that depends on the
-// sizes and the device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No atomics:
-// the same call gives the same bits.
+// sizes and the device alone adds its rows in order, k_colsum adds the blocks' partial rows in order.  No
+// atomics: the same call gives the same bits.
 #include <math.h>
 #include <string.h>
 
@@ -107,8 +107,8 @@ __device__ __forceinline__ void store_v(void *p, int64_t i, int bf16, float (&v)
   }
 }
 
-// A thread's values of a row: columns (256 c + thread) V .. + V - 1, c < NCH, below d <= kNormMaxD.  (A block of
-// fewer threads holds its row in c = 0.)  One branch on the type for all of a row's loads.
+// A thread's values of a row: columns (256 c + thread) V .. + V - 1, c < NCH, below d <= kNormMaxD.  (A
+// block of fewer threads holds its row in c = 0.)  One branch on the type for all of a row's loads.
 constexpr int kNormMaxThreads = 256;
 template <int V, int NCH>
 __device__ __forceinline__ void load_row(const void *p, int64_t first, int bf16, int d, float (&v)[NCH][V]) {
@@ -751,10 +751,10 @@ moe_status check_gate(const void *gate, int kind, int act, int dt, int64_t ld, i
   return MOE_OK;
 }
 
-// The ring of a kernel over n rows (word: where its errors go, the device's if NULL), or stages = 0 where it does not pay: rows that are not whole
-// 16-byte vectors, too long for two stages, or (backward) for the registers, or fewer than kRingRows
-// for each of the blocks that fill the device (1,180 x 2,048, fp32: 12.5 us against 10.5; 8,192 x
-// 4,096, bf16 with a gate of its own: 57 against 97).
+// The ring of a kernel over n rows (word: where its errors go, the device's if NULL), or stages = 0 where
+// it does not pay: rows that are not whole 16-byte vectors, too long for two stages, or (backward) for the
+// registers, or fewer than kRingRows for each of the blocks that fill the device (1,180 x 2,048, fp32:
+// 12.5 us against 10.5; 8,192 x 4,096, bf16 with a gate of its own: 57 against 97).
 constexpr int kRingBytes = 208 * 1024, kRingRows = 4, kMostBlocksPerSm = 16;
 struct RingPlan {
   Ring r{};

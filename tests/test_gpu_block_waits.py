@@ -97,7 +97,7 @@ def test_check_waits_for_every_stream(P, limit):
         limit(clocks)
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(100_000_000)  # 50 ms
+            torch.cuda._sleep(400_000_000)  # 0.2 s
             P.norm_in(x, w)
         assert not side.query()
         assert P.block_check() == status
