@@ -157,3 +157,27 @@ def test_the_next_call_reports(P, limit):
     for call in calls.values():
         call()
     assert P.block_check() == P.MOE_OK
+
+
+def test_first_call_inside_a_capture():
+    """The page of error words is pinned by the first call that may wait, which may be one that is captured."""
+    import subprocess
+    import sys
+    from pathlib import Path
+
+    code = """
+import torch
+import expert_ffn_gemv_b200 as P
+x, w = torch.randn(2000, 1024, device="cuda"), torch.randn(1024, device="cuda")
+a, m = torch.randn(40, 64, device="cuda").bfloat16(), (torch.randn(64, 64, device="cuda") / 8).bfloat16()
+torch.cuda.synchronize()
+for call in (lambda: P.norm_in(x, w), lambda: P.ffn_forward(a, m, m, m)):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call()
+    graph.replay()
+    assert torch.equal(y, call())
+assert P.block_check() == P.MOE_OK
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
